@@ -14,6 +14,10 @@
  *   a0  kvs_build_fathom_index  (data preparation) quantise a bf16 K cache to
  *                          the 4-bit channel-major bit-plane index
  *
+ * Beside it, a paged K/V cache for the layers that attend to every token or
+ * to a window (end of this file): kvs_paged_append, paged_decode_attn,
+ * paged_prompt_attn and kvs_paged_evict.
+ *
  * Sources (page title, then section):
  *   [FATHOM]   "Fathom: Per-Query Read Depth for Sparse Decoding over Offloaded
  *              KV Caches", abstract: a 4-bit K copy laid out channel by channel
@@ -430,6 +434,147 @@ KVS_API kvs_status kvs_selftest_scan_timeout(const kvs_fathom_index* ix, const k
 KVS_API kvs_status decode_step_timed(const kvs_decode_args* a, void* ws, size_t ws_bytes,
                                      int32_t* dev_status, void* stream, void* const* events,
                                      int32_t n_events);
+
+/* ---------------------------------------------------------------------------
+ * A paged K/V cache, and the operators over it: the layers around the sparse
+ * ones that attend to every cached token, or to a sliding window and a few
+ * first tokens. The pages define none of these calls.
+ *
+ * Token i of request r, KV head g has its rows in page
+ * id = table[r * table_ld + i / page] at
+ *   K + id * page_stride + g * head_stride + (i % page) * token_stride
+ * (elements; the same for V), D contiguous elements each. The strides let a
+ * pool be [num_pages][G][page][D], [num_pages][page][G][D], or a slice of a
+ * larger array; they are multiples of 8 and the pools 16-byte aligned. `page`
+ * is a power of two from 16 to 1024. n[r] is the number of tokens held
+ * (0 .. max_pages * page; outside that range it is clamped and KVS_EBOUNDS
+ * written to dev_status). Table entries behind a request's last page, and of
+ * pages that a call does not look at (behind a sliding window), are never
+ * read through: they may hold anything. An id outside 0 .. num_pages - 1 where
+ * a row is needed writes KVS_EBOUNDS to dev_status, and the rows of that page
+ * count as absent (not read, not written, not attended to).
+ * Requests may share pages that no call writes.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  uint16_t* K; /* bf16; written by kvs_paged_append and kvs_paged_evict only */
+  uint16_t* V;
+  int64_t page_stride, head_stride, token_stride; /* elements, of both pools */
+  const int32_t* table;                           /* device int32 [R][table_ld] */
+  int64_t table_ld;                               /* >= max_pages */
+  const int32_t* n;                               /* device int32 [R] */
+  int32_t R, G, D, page, max_pages, num_pages;    /* D must be 128 */
+} kvs_paged_kv;
+
+/* kvs_paged_append -- writes the newest tokens' rows into their pages. n[r]
+ * already counts them (all layers of a model share one n, advanced once a
+ * step): with c = cu[r+1] - cu[r] new tokens (cu device int32 [R+1], cu[0] = 0,
+ * ascending; NULL: one each, T = R), packed row cu[r] + t goes to position
+ * i = n[r] - c + t. Knew, Vnew bf16 [T][G][D] with rows new_ld elements apart
+ * from token to token (a multiple of 8) and D from head to head; packed rows
+ * from cu[R] on are not read. Positions outside 0 .. max_pages * page - 1 are
+ * not written (KVS_EBOUNDS). mass (nullable) f32 [R][G][max_pages * page] and
+ * pos (nullable) int32 of the same shape get, at i, 0 and the token's place in
+ * the request: seen[r] - c + t with seen (nullable device int32 [R]) the
+ * tokens that the request has had in all, these included; i without it. */
+KVS_API kvs_status kvs_paged_append(const kvs_paged_kv* kv, const uint16_t* Knew, const uint16_t* Vnew,
+                                    int64_t new_ld, const int32_t* cu, int32_t T, float* mass,
+                                    int32_t* pos, const int32_t* seen, int32_t* dev_status, void* stream);
+
+/* paged_decode_attn -- attention of each request's newest token (position
+ * n[r] - 1) over its cached tokens: for each (r, g, h < H), over the visible
+ * tokens j < n[r] (all of them with window = 0, otherwise those with
+ * j < sinks or j >= n[r] - window), l_j = scale * (q_h . K_j),
+ * out = sum_j softmax(l)_j V_j and lse = log sum_j exp(l_j). A request with no
+ * visible token gets out = 0 and lse = -inf.
+ *   q f32 or bf16 [R][G][H][D]; out f32 [R][G][H][D]; lse (nullable) f32
+ *   [R][G][H]. H in 1..8.
+ * mass, mass_out (both or neither) f32 [R][G][max_pages * page]: for every
+ * visible token mass_out[j] = mass[j] + sum_h softmax(l)_hj; the other entries
+ * of mass_out stay as they are. mass_out may be mass itself, or not overlap it.
+ * The softmax, the sums and the weights are f32; the products take q, K and V
+ * exactly and the weights to 24 bits.
+ * Workspace: kvs_paged_decode_workspace_size(R, G, H, weights ? max_pages *
+ * page : 0), independent of the lengths otherwise. */
+typedef struct {
+  const kvs_paged_kv* kv;
+  const void* q;
+  int32_t q_dtype, H, window, sinks;
+  float scale;
+  float* out;
+  float* lse;
+  const float* mass;
+  float* mass_out;
+} kvs_paged_decode_args;
+
+KVS_API kvs_status paged_decode_attn(const kvs_paged_decode_args* a, void* ws, size_t ws_bytes,
+                                     int32_t* dev_status, void* stream);
+KVS_API size_t kvs_paged_decode_workspace_size(int32_t R, int32_t G, int32_t H, int32_t weight_cap);
+
+/* paged_prompt_attn -- causal attention of the newest tokens of each request,
+ * a prompt or a chunk of one, over its cached tokens (their own rows are
+ * already in the cache). With c = cu[r+1] - cu[r] queries (cu device int32
+ * [R+1], cu[0] = 0, ascending), packed query cu[r] + t sits at position
+ * p = n[r] - c + t and sees the tokens j <= p, with window > 0 only those with
+ * j < sinks or j > p - window.
+ *   q bf16 [T][G*H][D] (query heads g*H .. g*H + H-1 share KV head g), tokens
+ *   q_ld elements apart; out bf16 likewise with out_ld; lse (nullable) f32
+ *   [T][G*H]. H in 1..8; q_ld, out_ld multiples of 8, q and out 16-byte
+ *   aligned. Packed rows from cu[R] on are neither read nor written; a query that sees
+ *   nothing (p < 0) gets out = 0 and lse = -inf.
+ * The softmax and all sums are f32; the weights are rounded to bf16 for the
+ * product with V, and out once at the end. A cached V row that is not finite
+ * makes the outputs of queries not finite that see it, and may those of
+ * queries up to 255 rows (token, head) before them; K and V rows that no
+ * query of a 256-row block sees have no influence on it. No workspace. */
+typedef struct {
+  const kvs_paged_kv* kv;
+  const uint16_t* q;
+  int64_t q_ld;
+  const int32_t* cu;
+  int32_t T, H, window, sinks;
+  float scale;
+  uint16_t* out;
+  int64_t out_ld;
+  float* lse;
+} kvs_paged_prompt_args;
+
+KVS_API kvs_status paged_prompt_attn(const kvs_paged_prompt_args* a, int32_t* dev_status, void* stream);
+
+/* kvs_paged_evict -- cuts every request that holds more than `budget` tokens
+ * down to `budget`, for each KV head by itself. Of the n[r] slots it keeps
+ * first those whose token's place pos is < sinks or >= seen[r] - recent (the
+ * lower slots, should places that repeat make them more than the budget), then
+ * those of largest mass (ties to the lower slot; NaN counts as lowest). Kept
+ * rows in slots >= budget move into the freed slots < budget, both in ascending
+ * order; no other row moves, so the order of the slots carries no meaning and
+ * pos says which token a slot holds.
+ *   mass f32, pos (nullable: slot i holds token i) int32
+ *   [R][G][max_pages * page]; seen (nullable: n) device int32 [R].
+ *   mass_out, pos_out (nullable with pos) of the same shape: entries
+ *   j < min(n[r], budget) get the values of the token now in slot j, the others
+ *   stay as they are. n_out int32 [R] = min(n[r], budget). Each may be its
+ *   input itself (in place), or not overlap it.
+ *   src (required) int32 [R][G][budget]: the slot that slot j's token was in,
+ *   -1 from n_out[r] on.
+ * budget >= 1, sinks, recent >= 0, sinks + recent <= budget. Pages behind
+ * n_out[r] are free afterwards. A page that moves rows must not be shared by
+ * two requests, nor be read by a call that runs at the same time.
+ * Workspace: kvs_paged_evict_workspace_size(). */
+typedef struct {
+  const kvs_paged_kv* kv;
+  const float* mass;
+  const int32_t* pos;
+  const int32_t* seen;
+  int32_t budget, sinks, recent;
+  float* mass_out;
+  int32_t* pos_out;
+  int32_t* n_out;
+  int32_t* src;
+} kvs_paged_evict_args;
+
+KVS_API kvs_status kvs_paged_evict(const kvs_paged_evict_args* a, void* ws, size_t ws_bytes,
+                                   int32_t* dev_status, void* stream);
+KVS_API size_t kvs_paged_evict_workspace_size(int32_t R, int32_t G, int32_t budget);
 
 #ifdef __cplusplus
 }

@@ -10,6 +10,7 @@ the library has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -62,6 +63,27 @@ class DecodeArgsC(ctypes.Structure):
                 ("idx", P), ("slots", P), ("misses", P)]
 
 
+class PagedKVC(ctypes.Structure):
+    _fields_ = [("K", P), ("V", P), ("page_stride", I64), ("head_stride", I64), ("token_stride", I64),
+                ("table", P), ("table_ld", I64), ("n", P), ("R", I32), ("G", I32), ("D", I32), ("page", I32),
+                ("max_pages", I32), ("num_pages", I32)]
+
+
+class PagedDecodeArgsC(ctypes.Structure):
+    _fields_ = [("kv", ctypes.POINTER(PagedKVC)), ("q", P), ("q_dtype", I32), ("H", I32), ("window", I32),
+                ("sinks", I32), ("scale", F32), ("out", P), ("lse", P), ("mass", P), ("mass_out", P)]
+
+
+class PagedPromptArgsC(ctypes.Structure):
+    _fields_ = [("kv", ctypes.POINTER(PagedKVC)), ("q", P), ("q_ld", I64), ("cu", P), ("T", I32), ("H", I32),
+                ("window", I32), ("sinks", I32), ("scale", F32), ("out", P), ("out_ld", I64), ("lse", P)]
+
+
+class PagedEvictArgsC(ctypes.Structure):
+    _fields_ = [("kv", ctypes.POINTER(PagedKVC)), ("mass", P), ("pos", P), ("seen", P), ("budget", I32),
+                ("sinks", I32), ("recent", I32), ("mass_out", P), ("pos_out", P), ("n_out", P), ("src", P)]
+
+
 def _declare():
     L = _lib
     L.kvs_abi_version.restype = I32
@@ -100,6 +122,18 @@ def _declare():
     L.kvs_selftest_scan_timeout.argtypes = [ctypes.POINTER(FathomIndexC), ctypes.POINTER(PlanC), P, I32,
                                             P, I64, P, P]
     L.kvs_selftest_scan_timeout.restype = I32
+    L.kvs_paged_append.argtypes = [ctypes.POINTER(PagedKVC), P, P, I64, P, I32, P, P, P, P, P]
+    L.kvs_paged_append.restype = I32
+    L.paged_decode_attn.argtypes = [ctypes.POINTER(PagedDecodeArgsC), P, SZ, P, P]
+    L.paged_decode_attn.restype = I32
+    L.kvs_paged_decode_workspace_size.argtypes = [I32, I32, I32, I32]
+    L.kvs_paged_decode_workspace_size.restype = SZ
+    L.paged_prompt_attn.argtypes = [ctypes.POINTER(PagedPromptArgsC), P, P]
+    L.paged_prompt_attn.restype = I32
+    L.kvs_paged_evict.argtypes = [ctypes.POINTER(PagedEvictArgsC), P, SZ, P, P]
+    L.kvs_paged_evict.restype = I32
+    L.kvs_paged_evict_workspace_size.argtypes = [I32, I32, I32]
+    L.kvs_paged_evict_workspace_size.restype = SZ
 
 
 _declare()
@@ -520,3 +554,205 @@ def decode_step(q, index: FathomIndex, n, B: int, k: int, fullK, fullV, slot_map
                       q_dtype=q.dtype)
     step(q, idx_in=idx_in, idx_shared=idx_shared, stream=stream)
     return step.out, step.lse, step.idx, step.slots, step.misses, step.plan
+
+
+# ----------------------------------------------------------------------------- the paged K/V cache
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on(dev: torch.device, stream):
+    """The context a call runs in: its tensors' device current and, where one is given, `stream`
+    current too, so that what the call allocates belongs to the stream that uses it."""
+    if stream is not None:
+        _require(stream.device == dev, f"the stream is on {stream.device}, the cache on {dev}")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() == dev.index:
+        return _SAME_DEVICE
+    return torch.cuda.device(dev)
+
+
+def _need(name: str, t, shape, dtype, dev):
+    """t is a contiguous tensor of this shape and type on dev."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.device != dev \
+            or not t.is_contiguous():
+        what = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else repr(type(t))
+        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {dev}, got {what}")
+    return t
+
+
+def _counts(**values):
+    """Every value fits the C boundary's int32 and is not negative."""
+    for name, v in values.items():
+        _require(isinstance(v, int) and 0 <= v < 2 ** 31, f"{name} must be an int from 0 to 2^31 - 1, got {v!r}")
+
+
+class PagedKV:
+    """A paged K/V cache (tensors owned by torch).
+
+    k_pages, v_pages bf16 [num_pages][G][page][128], of the same strides, the last dimension contiguous
+    (a pool laid out [num_pages][page][G][128] is passed as its .transpose(1, 2)); table int32
+    [R][max_pages], the pages of each request in order; n int32 [R], the tokens each holds. The tensors
+    are read by later calls as they are then: n and table may change in place, in a captured graph too.
+    """
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, n: torch.Tensor):
+        for name, t, dt, dims in (("k_pages", k_pages, torch.bfloat16, 4), ("v_pages", v_pages, torch.bfloat16, 4),
+                                  ("table", table, torch.int32, 2), ("n", n, torch.int32, 1)):
+            _require(isinstance(t, torch.Tensor) and t.dtype == dt and t.dim() == dims,
+                     f"{name} must be a {dt} tensor of {dims} dimensions")
+            _require(t.device == k_pages.device and t.is_cuda, f"{name} must be on k_pages' CUDA device")
+            _require(t.stride(-1) == 1 or t.shape[-1] == 1, f"{name} must be contiguous in its last dimension")
+        _require(k_pages.shape == v_pages.shape and k_pages.stride() == v_pages.stride(),
+                 "k_pages and v_pages must have the same shape and strides")
+        self.num_pages, self.G, self.page, self.D = k_pages.shape
+        self.R, self.max_pages = table.shape
+        _require(n.shape[0] == self.R, f"n must have {self.R} entries, got {n.shape[0]}")
+        self.k_pages, self.v_pages, self.table, self.n = k_pages, v_pages, table, n
+        self.device = k_pages.device
+        self.cap = self.max_pages * self.page
+        # the stride of a dimension of one entry says nothing
+        st = [x if k > 1 else self.D for x, k in zip(k_pages.stride(), k_pages.shape)]
+        self._c = PagedKVC(k_pages.data_ptr(), v_pages.data_ptr(), st[0], st[1], st[2], table.data_ptr(),
+                           table.stride(0) if self.R > 1 else self.max_pages, n.data_ptr(), self.R, self.G, self.D,
+                           self.page, self.max_pages, self.num_pages)
+        self._ref = ctypes.pointer(self._c)
+
+    def _state(self, name, t, dtype):
+        return None if t is None else _need(name, t, (self.R, self.G, self.cap), dtype, self.device).data_ptr()
+
+
+def paged_append(cache: PagedKV, Knew: torch.Tensor, Vnew: torch.Tensor, cu=None, mass=None, pos=None, seen=None,
+                 stream=None, dev_status=None):
+    """Writes the newest tokens' rows into their pages (kvs_paged_append): Knew, Vnew bf16 [T][G][128],
+    packed by request with cu int32 [R+1] (None: one token each). cache.n already counts them. mass f32 and
+    pos int32 [R][G][cap] get 0 and the token's place (counted by seen int32 [R])."""
+    dev = cache.device
+    _require(Knew.dim() == 3 and Knew.shape == Vnew.shape and Knew.shape[1:] == (cache.G, cache.D)
+             and Knew.dtype == Vnew.dtype == torch.bfloat16 and Knew.device == Vnew.device == dev,
+             f"Knew and Vnew must be bf16 [T][{cache.G}][{cache.D}] on {dev}")
+    st = Knew.stride()
+    _require(Vnew.stride() == st and st[2] == 1 and (st[1] == cache.D or cache.G == 1),
+             "Knew and Vnew must have the same strides, their heads contiguous")
+    T = Knew.shape[0]
+    ld = st[0] if T > 1 else cache.G * cache.D
+    cup = None if cu is None else _need("cu", cu, (cache.R + 1,), torch.int32, dev).data_ptr()
+    sp = None if seen is None else _need("seen", seen, (cache.R,), torch.int32, dev).data_ptr()
+    mp, pp = cache._state("mass", mass, torch.float32), cache._state("pos", pos, torch.int32)
+    with _on(dev, stream):
+        _check(_lib.kvs_paged_append(cache._ref, Knew.data_ptr(), Vnew.data_ptr(), ld, cup, T, mp, pp, sp,
+                                     _ptr(dev_status), torch.cuda.current_stream(dev).cuda_stream),
+               "kvs_paged_append")
+
+
+def paged_decode_workspace(cache: PagedKV, H: int, weights: bool = False) -> torch.Tensor:
+    """A workspace for paged_decode_attn, for callers that keep one (calls that may run at the same time
+    need one each)."""
+    nb = _lib.kvs_paged_decode_workspace_size(cache.R, cache.G, H, cache.cap if weights else 0)
+    return torch.empty(max(int(nb), 16), dtype=torch.uint8, device=cache.device)
+
+
+def paged_decode_attn(q: torch.Tensor, cache: PagedKV, window: int = 0, sinks: int = 0, scale: float | None = None,
+                      out=None, lse=None, mass=None, mass_out=None, ws=None, stream=None, dev_status=None):
+    """Attention of each request's newest token over its cache: q f32/bf16 [R][G][H][128] -> (out f32
+    [R][G][H][128], lse f32 [R][G][H]). window > 0: only the last `window` tokens and the first `sinks`.
+    mass f32 [R][G][cap]: every visible token's softmax weights, summed over the H heads, are added to it
+    (in place, or into mass_out)."""
+    dev, R, G = cache.device, cache.R, cache.G
+    _counts(window=window, sinks=sinks)
+    H = q.shape[2] if q.dim() == 4 else 0
+    qd = q.dtype
+    if qd != torch.bfloat16:
+        qd = torch.float32
+    _need("q", q, (R, G, H, cache.D), qd, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(R, G, H, cache.D, dtype=torch.float32, device=dev)
+        else:
+            _need("out", out, (R, G, H, cache.D), torch.float32, dev)
+        if lse is None:
+            lse = torch.empty(R, G, H, dtype=torch.float32, device=dev)
+        else:
+            _need("lse", lse, (R, G, H), torch.float32, dev)
+        mp = cache._state("mass", mass, torch.float32)
+        mo = mp if mass_out is None else cache._state("mass_out", mass_out, torch.float32)
+        if ws is None:
+            ws = paged_decode_workspace(cache, H, mass is not None)
+        else:
+            _require(ws.device == dev and ws.dtype == torch.uint8 and ws.is_contiguous(),
+                     f"ws must be a contiguous uint8 tensor on {dev}")
+        a = PagedDecodeArgsC(cache._ref, q.data_ptr(), KVS_BF16 if qd == torch.bfloat16 else KVS_F32, H, window,
+                             sinks, 1.0 / math.sqrt(cache.D) if scale is None else scale, out.data_ptr(),
+                             lse.data_ptr(), mp, mo)
+        _check(_lib.paged_decode_attn(ctypes.byref(a), ws.data_ptr(), ws.numel(), _ptr(dev_status),
+                                      torch.cuda.current_stream(dev).cuda_stream), "paged_decode_attn")
+    return out, lse
+
+
+def paged_prompt_attn(q: torch.Tensor, cu: torch.Tensor, cache: PagedKV, window: int = 0, sinks: int = 0,
+                      scale: float | None = None, out=None, lse=None, stream=None, dev_status=None):
+    """Causal attention of the newest tokens of each request over its cache: q bf16 [T][G*H][128], packed by
+    request with cu int32 [R+1] -> (out bf16 [T][G*H][128], lse f32 [T][G*H]). window > 0: each token sees
+    itself and the window - 1 before it, and the first `sinks`. Rows from cu[R] on are left as they are
+    (zero in an `out` and `lse` made here)."""
+    dev = cache.device
+    _require(q.dim() == 3 and q.dtype == torch.bfloat16 and q.device == dev and q.shape[2] == cache.D
+             and q.shape[1] % cache.G == 0, f"q must be bf16 [T][{cache.G}*H][{cache.D}] on {dev}")
+    _counts(window=window, sinks=sinks)
+    T, Hq, D = q.shape
+    _need("cu", cu, (cache.R + 1,), torch.int32, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device=dev)
+        else:
+            _require(out.shape == q.shape and out.dtype == torch.bfloat16 and out.device == dev,
+                     f"out must be bf16 {tuple(q.shape)} on {dev}")
+        for name, t in (("q", q), ("out", out)):
+            _require(t.stride(2) == 1 and (t.stride(1) == D or Hq == 1), f"{name} must have contiguous heads")
+        if lse is None:
+            lse = torch.zeros(T, Hq, dtype=torch.float32, device=dev)
+        else:
+            _need("lse", lse, (T, Hq), torch.float32, dev)
+        ld = (q.stride(0), out.stride(0)) if T > 1 else (Hq * D, Hq * D)
+        a = PagedPromptArgsC(cache._ref, q.data_ptr(), ld[0], cu.data_ptr(), T, Hq // cache.G, window, sinks,
+                             1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), ld[1], lse.data_ptr())
+        _check(_lib.paged_prompt_attn(ctypes.byref(a), _ptr(dev_status), torch.cuda.current_stream(dev).cuda_stream),
+               "paged_prompt_attn")
+    return out, lse
+
+
+def paged_evict(cache: PagedKV, mass: torch.Tensor, budget: int, sinks: int = 0, recent: int = 0, pos=None,
+                seen=None, mass_out=None, pos_out=None, n_out=None, src=None, ws=None, stream=None,
+                dev_status=None) -> torch.Tensor:
+    """Cuts every request that holds more than `budget` tokens down to `budget`, for each KV head by itself
+    (kvs_paged_evict): kept are tokens placed (pos int32 [R][G][cap]; None: slot i holds token i) before
+    `sinks` or among the last `recent` of the `seen` int32 [R] (None: cache.n), then those of largest mass f32
+    [R][G][cap]. Kept rows behind the budget move into freed slots; mass, pos and cache.n are updated in
+    place unless mass_out, pos_out and n_out are given. -> src int32 [R][G][budget]: the slot each token was
+    in (-1 behind the last)."""
+    dev = cache.device
+    _counts(budget=budget, sinks=sinks, recent=recent)
+    with _on(dev, stream):
+        mp = cache._state("mass", mass, torch.float32)
+        _require(mp is not None, "mass is required")
+        mo = mp if mass_out is None else cache._state("mass_out", mass_out, torch.float32)
+        pp = cache._state("pos", pos, torch.int32)
+        _require(pp is not None or pos_out is None, "pos_out without pos")
+        po = pp if pos_out is None else cache._state("pos_out", pos_out, torch.int32)
+        sp = None if seen is None else _need("seen", seen, (cache.R,), torch.int32, dev).data_ptr()
+        no = (cache.n if n_out is None else _need("n_out", n_out, (cache.R,), torch.int32, dev)).data_ptr()
+        _require(budget >= 1, "budget must be at least 1")
+        if src is None:
+            src = torch.empty(cache.R, cache.G, budget, dtype=torch.int32, device=dev)
+        else:
+            _need("src", src, (cache.R, cache.G, budget), torch.int32, dev)
+        if ws is None:
+            nb = _lib.kvs_paged_evict_workspace_size(cache.R, cache.G, budget)
+            ws = torch.empty(max(int(nb), 16), dtype=torch.uint8, device=dev)
+        else:
+            _require(ws.device == dev and ws.dtype == torch.uint8 and ws.is_contiguous(),
+                     f"ws must be a contiguous uint8 tensor on {dev}")
+        a = PagedEvictArgsC(cache._ref, mp, pp, sp, budget, sinks, recent, mo, po, no, src.data_ptr())
+        _check(_lib.kvs_paged_evict(ctypes.byref(a), ws.data_ptr(), ws.numel(), _ptr(dev_status),
+                                    torch.cuda.current_stream(dev).cuda_stream), "kvs_paged_evict")
+    return src

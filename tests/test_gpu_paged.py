@@ -1,0 +1,642 @@
+"""The paged K/V cache's operators on the GPU, against their definitions in 64
+bits (tests/_paged.py: the tolerances are derived there)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import _paged as ref
+
+pytestmark = pytest.mark.gpu
+D = 128
+DEV = "cuda"
+SC = 1 / math.sqrt(D)
+
+
+@pytest.fixture(scope="module")
+def kvs():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    import kv_index_scan_b200
+    return kv_index_scan_b200
+
+
+def _bits(t):
+    return t.contiguous().view(torch.int16) if t.dtype == torch.bfloat16 else t
+
+
+def _status():
+    return torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+# ----------------------------------------------------------------------------- append
+
+@pytest.mark.parametrize("layout", ["head", "token", "both"])
+@pytest.mark.parametrize("G,page", [(1, 16), (3, 32), (8, 64), (5, 1024)])
+def test_append_writes_its_rows_and_no_others(kvs, layout, G, page):
+    lens, new = [5, 40, 0, 333, 17], [5, 3, 0, 300, 1]
+    k, v, table, n = ref.make(lens, G, page, seed=page, layout=layout)
+    cache = kvs.PagedKV(k, v, table, n)
+    cu = torch.tensor([0] + list(np.cumsum(new)), dtype=torch.int32, device=DEV)
+    T = int(cu[-1]) + 4  # padded rows behind the last request
+    rows = torch.randn(T, 2 * G * D + 8, device=DEV).to(torch.bfloat16)  # rows inside a wider projection
+    Kn, Vn = rows[:, :G * D].view(T, G, D), rows[:, G * D:2 * G * D].view(T, G, D)
+    mass = torch.full((5, G, cache.cap), 7.0, device=DEV)
+    pos = torch.full((5, G, cache.cap), -9, dtype=torch.int32, device=DEV)
+    seen = n + 1000
+    wk, wv, wm, wp = k.clone(), v.clone(), mass.clone(), pos.clone()
+    st = _status()
+    kvs.paged_append(cache, Kn, Vn, cu, mass=mass, pos=pos, seen=seen, dev_status=st)
+    for r, (m, c) in enumerate(zip(lens, new)):
+        for t in range(c):
+            i = m - c + t
+            pg = int(table[r, i // page])
+            wk[pg, :, i % page], wv[pg, :, i % page] = Kn[cu[r] + t], Vn[cu[r] + t]
+            wm[r, :, i], wp[r, :, i] = 0.0, 1000 + i
+    assert torch.equal(_bits(k), _bits(wk)) and torch.equal(_bits(v), _bits(wv))
+    assert torch.equal(mass, wm) and torch.equal(pos, wp) and int(st) == 0
+
+
+def test_append_one_token_each(kvs):
+    lens = [1, 16, 17, 100]
+    k, v, table, n = ref.make(lens, 4, 16, seed=2)
+    cache = kvs.PagedKV(k, v, table, n)
+    Kn, Vn = torch.randn(2, 4, 4, D, device=DEV).to(torch.bfloat16)
+    pos = torch.full((4, 4, cache.cap), -9, dtype=torch.int32, device=DEV)
+    kvs.paged_append(cache, Kn, Vn, pos=pos)
+    for r, m in enumerate(lens):
+        pg = int(table[r, (m - 1) // 16])
+        assert torch.equal(k[pg, :, (m - 1) % 16], Kn[r]) and torch.equal(v[pg, :, (m - 1) % 16], Vn[r])
+        assert bool((pos[r, :, m - 1] == m - 1).all()) and bool((pos[r, :, m:] == -9).all())
+
+
+def test_append_refuses_positions_and_pages_that_are_none(kvs):
+    """A full cache, more new tokens than the length counts, and a bad page id: nothing is written there and
+    the status word says so."""
+    k, v, table, n = ref.make([48, 2, 20], 2, 16, seed=3, slack=0)
+    cache = kvs.PagedKV(k, v, table, n)
+    cap = cache.cap
+    n.copy_(torch.tensor([cap + 1, 1, 20]))
+    table[2, 1] = cache.num_pages
+    wk, wv = k.clone(), v.clone()
+    cu = torch.tensor([0, 1, 3, 4], dtype=torch.int32, device=DEV)
+    Kn, Vn = torch.ones(2, 4, 2, D, device=DEV).to(torch.bfloat16)
+    st = _status()
+    kvs.paged_append(cache, Kn, Vn, cu, dev_status=st)
+    wk[int(table[1, 0]), :, 0], wv[int(table[1, 0]), :, 0] = 1, 1  # the second of the two tokens fits
+    assert int(st) == kvs.KVS_EBOUNDS
+    assert torch.equal(_bits(k), _bits(wk)) and torch.equal(_bits(v), _bits(wv))
+
+
+def test_append_many_requests(kvs):
+    """More requests than a warp's search step, with runs of empty ones."""
+    rng = np.random.default_rng(5)
+    new = [int(x) for x in rng.integers(0, 4, 1100)]
+    new[300:400] = [0] * 100
+    new[-1] = 2
+    k, v, table, n = ref.make(new, 1, 16, seed=5, slack=0, spare=0)
+    cache = kvs.PagedKV(k, v, table, n)
+    cu = torch.tensor([0] + list(np.cumsum(new)), dtype=torch.int32, device=DEV)
+    T = int(cu[-1])
+    Kn, Vn = torch.randn(2, T, 1, D, device=DEV).to(torch.bfloat16)
+    kvs.paged_append(cache, Kn, Vn, cu)
+    row = torch.repeat_interleave(torch.arange(len(new)), torch.tensor(new)).to(DEV)
+    at = torch.arange(T, device=DEV) - cu[row.long()]
+    pg = table[row, at // 16].long()
+    assert torch.equal(k[pg, 0, at % 16], Kn[:, 0]) and torch.equal(v[pg, 0, at % 16], Vn[:, 0])
+
+
+# ----------------------------------------------------------------------------- decode
+
+LENS = [0, 1, 15, 16, 17, 63, 64, 65, 127, 129, 300, 1031]
+
+
+@pytest.mark.parametrize("H", [1, 2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("qdt", [torch.bfloat16, torch.float32])
+def test_decode_head_counts_and_lengths(kvs, H, qdt):
+    k, v, table, n = ref.make(LENS, 2, 16, seed=H)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(len(LENS), 2, H, D, device=DEV).to(qdt)
+    st = _status()
+    out, lse = kvs.paged_decode_attn(q, cache, dev_status=st)
+    ref.check_decode(out, lse, q, k, v, table, LENS, 0, 0, SC)
+    assert int(st) == 0
+
+
+@pytest.mark.parametrize("layout", ["head", "token", "both"])
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256, 1024])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (0, 3), (1, 0), (1, 1), (64, 4), (100, 70), (513, 16), (5000, 4)])
+def test_decode_pages_windows_and_weights(kvs, layout, page, window, sinks):
+    """Rows behind the last token and pages that the window has passed hold NaN; the weights add up beside."""
+    lens = [1, 70, 517, 1030, 2049]
+    G, H = 3, 4
+    k, v, table, n = ref.make(lens, G, page, seed=page + window, layout=layout)
+    for r, m in enumerate(lens):
+        vis = set((ref.visible(m - 1, window, sinks)).tolist())
+        for j in range(m):
+            if j not in vis:
+                k[int(table[r, j // page]), :, j % page] = float("nan")
+                v[int(table[r, j // page]), :, j % page] = float("inf")
+        for p in range(-(-m // page)):
+            if not any(j in vis for j in range(p * page, min(m, (p + 1) * page))):
+                table[r, p] = -1  # released
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(len(lens), G, H, D, device=DEV).to(torch.bfloat16)
+    mass = torch.rand(len(lens), G, cache.cap, device=DEV)
+    before = mass.clone()
+    kt, vt, tt = k.nan_to_num(0, 0, 0), v.nan_to_num(0, 0, 0), table.clamp(min=0)
+    st = _status()
+    out, lse = kvs.paged_decode_attn(q, cache, window, sinks, mass=mass, dev_status=st)
+    ref.check_decode(out, lse, q, kt, vt, tt, lens, window, sinks, SC, before, mass)
+    # out of place, entries that are not visible stay
+    mo = torch.full_like(before, float("nan"))
+    out2, lse2 = kvs.paged_decode_attn(q, cache, window, sinks, mass=before, mass_out=mo, dev_status=st)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2) and int(st) == 0
+    for r, m in enumerate(lens):
+        vis = torch.zeros(cache.cap, dtype=torch.bool, device=DEV)
+        vis[torch.from_numpy(ref.visible(m - 1, window, sinks)).to(DEV)] = True
+        assert torch.equal(mo[r][:, vis], mass[r][:, vis]) and bool(torch.isnan(mo[r][:, ~vis]).all())
+
+
+@pytest.mark.parametrize("R,G,n_", [(1, 1, 40001), (1, 8, 9000), (3, 2, 30011), (257, 3, 90), (40, 8, 700)])
+def test_decode_splits(kvs, R, G, n_):
+    """One long row over every block, and more rows than blocks."""
+    rng = np.random.default_rng(R)
+    lens = [n_] + [int(x) for x in rng.integers(0, n_ + 1, R - 1)]
+    k, v, table, n = ref.make(lens, G, 64, seed=R, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(R, G, 4, D, device=DEV)
+    mass = torch.zeros(R, G, cache.cap, device=DEV)
+    out, lse = kvs.paged_decode_attn(q, cache, mass=mass)
+    ref.check_decode(out, lse, q, k, v, table, lens, 0, 0, SC, torch.zeros_like(mass), mass)
+
+
+def test_decode_extreme_logits(kvs):
+    """Logits from -3e4 to 3e4 and equal ones: the running maximum carries every one."""
+    lens = [700, 700]
+    k, v, table, n = ref.make(lens, 1, 16, seed=8)
+    kt = k.clone()
+    for j in range(700):
+        pg = int(table[0, j // 16])
+        k[pg, 0, j % 16] = 0.0
+        k[pg, 0, j % 16, 0] = float((j * 37) % 700 - 350)
+        k[int(table[1, j // 16]), 0, j % 16] = 1.0
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.zeros(2, 1, 2, D, device=DEV)
+    q[0, 0, 0, 0], q[0, 0, 1, 0], q[1] = 1000.0, -1000.0, 0.5
+    out, lse = kvs.paged_decode_attn(q, cache)
+    ref.check_decode(out, lse, q, k, v, table, lens, 0, 0, SC)
+    assert kt.shape == k.shape
+
+
+def test_decode_bad_pages_and_lengths(kvs):
+    """A page id that is none in a visible place, and lengths out of range: the page's tokens count as absent,
+    the length is clamped, and the status word says so."""
+    lens = [40, 64, 10]
+    k, v, table, n = ref.make(lens, 2, 16, seed=4, slack=0, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    good = table.clone()
+    table[0, 1] = cache.num_pages + 5
+    n.copy_(torch.tensor([40, 1 << 20, -3]))
+    q = torch.randn(3, 2, 4, D, device=DEV)
+    st = _status()
+    mass = torch.zeros(3, 2, cache.cap, device=DEV)
+    out, lse = kvs.paged_decode_attn(q, cache, mass=mass, dev_status=st)
+    assert int(st) == kvs.KVS_EBOUNDS
+    K, V = ref.tokens(k, good, 0, 40), ref.tokens(v, good, 0, 40)
+    some = [j for j in range(40) if j // 16 != 1]
+    for g in range(2):
+        o, ls, w, e, va = ref.attend(q[0, g].double(), K[some][:, g], V[some][:, g], SC)
+        assert float((out[0, g] - o).abs().max()) < 1e-4 and float((lse[0, g] - ls).abs().max()) < 1e-4
+    assert bool((mass[0, :, 16:32] == 0).all())
+    ref.check_decode(out[1:2], lse[1:2], q[1:2], k, v, good[1:2], [64], 0, 0, SC)
+    assert bool((out[2] == 0).all()) and bool(torch.isneginf(lse[2]).all())
+
+
+def test_decode_offsets_past_32_bits(kvs):
+    """A pool of more than 2^32 bytes and 2^31 elements, its last pages in use."""
+    P, G, page = 270_000, 8, 16  # 4.4e9 elements a pool
+    k = torch.empty(P, G, page, D, dtype=torch.bfloat16, device=DEV)
+    v = torch.empty_like(k)
+    lens = [100]
+    table = torch.tensor([[P - 1, 3, P - 2, P // 2, P - 7, 0, P - 3]], dtype=torch.int32, device=DEV)
+    for p in table[0].tolist():
+        k[p], v[p] = torch.randn(2, G, page, D, device=DEV).to(torch.bfloat16)
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(1, G, 4, D, device=DEV).to(torch.bfloat16)
+    out, lse = kvs.paged_decode_attn(q, cache)
+    ref.check_decode(out, lse, q, k, v, table, lens, 0, 0, SC)
+    qp = torch.randn(100, G * 4, D, device=DEV).to(torch.bfloat16)
+    cu = torch.tensor([0, 100], dtype=torch.int32, device=DEV)
+    po, pl = kvs.paged_prompt_attn(qp, cu, cache)
+    ref.check_prompt(po, pl, qp, [0, 100], k, v, table, lens, 0, 0, SC, G)
+    Kn, Vn = torch.randn(2, 1, G, D, device=DEV).to(torch.bfloat16)
+    kvs.paged_append(cache, Kn, Vn)
+    assert torch.equal(k[P - 3, :, 3], Kn[0]) and torch.equal(v[P - 3, :, 3], Vn[0])
+    want = ref.tokens(k, table, 0, 100)
+    src = kvs.paged_evict(cache, torch.rand(1, G, cache.cap, device=DEV), 20)
+    got = ref.tokens(k, table, 0, 20)
+    for g in range(G):
+        assert torch.equal(got[:, g], want[src[0, g].long(), g])
+
+
+def test_decode_caller_buffers_streams_and_graph(kvs):
+    """Caller's outputs and workspace; two calls at once on two streams; a captured call replayed after the
+    lengths, the table and the queries changed in place."""
+    lens = [500, 90]
+    k, v, table, n = ref.make(lens, 2, 16, seed=6, poison=False, slack=4)
+    cache = kvs.PagedKV(k, v, table, n)
+    qs = [torch.randn(2, 2, 4, D, device=DEV) for _ in range(2)]
+    want = [kvs.paged_decode_attn(q, cache) for q in qs]
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got.append([kvs.paged_decode_attn(q, cache, stream=s) for q, s in zip(qs, side)])
+    torch.cuda.synchronize()
+    for pair in got:
+        for (o, l), (wo, wl) in zip(pair, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+    q, out, lse = qs[0].clone(), torch.empty(2, 2, 4, D, device=DEV), torch.empty(2, 2, 4, device=DEV)
+    ws = kvs.paged_decode_workspace(cache, 4)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvs.paged_decode_attn(q, cache, window=200, sinks=2, out=out, lse=lse, ws=ws)
+    for m in ([500, 90], [333, 1], [0, 77]):
+        n.copy_(torch.tensor(m))
+        q.normal_()
+        graph.replay()
+        ref.check_decode(out, lse, q, k, v, table, m, 200, 2, SC)
+
+
+def test_binding_refusals(kvs):
+    k, v, table, n = ref.make([20], 2, 16, seed=1)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(1, 2, 4, D, device=DEV)
+    cu = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    bad = [lambda: kvs.paged_decode_attn(q[:, :1], cache), lambda: kvs.paged_decode_attn(q.half(), cache),
+           lambda: kvs.paged_decode_attn(q, cache, window=-1), lambda: kvs.paged_decode_attn(q, cache, window=2 ** 32),
+           lambda: kvs.paged_decode_attn(q, cache, out=torch.empty(1, 2, 4, D)),
+           lambda: kvs.paged_decode_attn(q, cache, mass=torch.zeros(1, 2, cache.cap + 1, device=DEV)),
+           lambda: kvs.paged_decode_attn(q, cache, ws=torch.empty(16, device=DEV)),
+           lambda: kvs.paged_prompt_attn(q.view(1, 8, D), cu, cache),
+           lambda: kvs.paged_prompt_attn(q.view(1, 8, D).bfloat16(), cu.long(), cache),
+           lambda: kvs.paged_prompt_attn(q.view(1, 8, D).bfloat16()[:, :7], cu, cache),
+           lambda: kvs.paged_append(cache, q[:, :, 0], q[:, :, 1]),
+           lambda: kvs.paged_evict(cache, torch.zeros(1, 2, cache.cap, device=DEV), 0),
+           lambda: kvs.paged_evict(cache, torch.zeros(1, 2, cache.cap, device=DEV), 8, pos_out=torch.zeros(1)),
+           lambda: kvs.PagedKV(k, v[:, :, ::2], table, n), lambda: kvs.PagedKV(k, v, table.long(), n),
+           lambda: kvs.PagedKV(k, v, table, n[:0])]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was accepted")
+    for call in (lambda: kvs.paged_decode_attn(torch.randn(1, 2, 9, D, device=DEV), cache),
+                 lambda: kvs.paged_evict(cache, torch.zeros(1, 2, cache.cap, device=DEV), 8, sinks=5, recent=4),
+                 lambda: kvs.paged_append(cache, k[:2, :, 0].contiguous(), k[:2, :, 0].contiguous())):
+        with pytest.raises(kvs.KvsError):
+            call()
+
+
+# ----------------------------------------------------------------------------- prompt
+
+def _prompt(kvs, lens, new, G, H, page, window, sinks, seed=0, pad=3, layout="head", poison=True):
+    k, v, table, n = ref.make(lens, G, page, seed=seed, layout=layout, poison=poison)
+    cache = kvs.PagedKV(k, v, table, n)
+    cu = [0] + [int(x) for x in np.cumsum(new)]
+    T = cu[-1] + pad
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    q = torch.randn(T, G * H, D, generator=g, device=DEV).to(torch.bfloat16)
+    out = torch.full((T, G * H, D), 3.5, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((T, G * H), -7.25, device=DEV)
+    st = _status()
+    kvs.paged_prompt_attn(q, torch.tensor(cu, dtype=torch.int32, device=DEV), cache, window, sinks, out=out, lse=lse,
+                          dev_status=st)
+    ref.check_prompt(out, lse, q, cu, k, v, table, lens, window, sinks, SC, G)
+    assert bool((out[cu[-1]:] == 3.5).all()) and bool((lse[cu[-1]:] == -7.25).all()), "rows behind the last request"
+    assert int(st) == 0
+
+
+@pytest.mark.parametrize("H", [1, 2, 3, 4, 5, 6, 7, 8])
+def test_prompt_head_counts(kvs, H):
+    _prompt(kvs, [1, 2, 130, 515, 64], [1, 2, 130, 300, 1], 2, H, 16, 0, 0, seed=H)
+
+
+@pytest.mark.parametrize("page", [16, 64, 128, 1024])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (1, 2), (17, 5), (128, 4), (129, 130), (600, 1), (4000, 4)])
+@pytest.mark.parametrize("layout", ["head", "token"])
+def test_prompt_windows(kvs, page, window, sinks, layout):
+    _prompt(kvs, [700, 1301, 31], [700, 257, 0], 1, 4, page, window, sinks, seed=window, layout=layout)
+
+
+@pytest.mark.parametrize("lens,new", [([0], [0]), ([1], [1]), ([2000], [1]), ([900, 0, 0, 40], [900, 0, 0, 40]),
+                                      ([127, 128, 129], [127, 128, 129]), ([255, 256, 257], [255, 256, 257])])
+def test_prompt_lengths(kvs, lens, new):
+    _prompt(kvs, lens, new, 2, 2, 16, 0, 0, seed=len(lens))
+
+
+def test_prompt_long(kvs):
+    _prompt(kvs, [4500], [4500], 1, 2, 64, 0, 0, seed=1)
+    _prompt(kvs, [4500], [2000], 1, 2, 64, 1000, 4, seed=2)
+
+
+def test_prompt_many_requests(kvs):
+    rng = np.random.default_rng(1)
+    new = [int(x) for x in rng.integers(0, 9, 300)]
+    _prompt(kvs, [x + int(y) for x, y in zip(new, rng.integers(0, 50, 300))], new, 1, 3, 16, 0, 0, seed=4)
+
+
+def test_prompt_queries_before_the_first_token(kvs):
+    """More queries than tokens: those in front of the first see nothing."""
+    k, v, table, n = ref.make([3], 1, 16, seed=9)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(5, 2, D, device=DEV).to(torch.bfloat16)
+    out, lse = kvs.paged_prompt_attn(q, torch.tensor([0, 5], dtype=torch.int32, device=DEV), cache)
+    ref.check_prompt(out, lse, q, [0, 5], k, v, table, [3], 0, 0, SC, 1)
+    assert bool((out[:2] == 0).all()) and bool(torch.isneginf(lse[:2]).all())
+
+
+def test_prompt_released_pages_and_strided_rows(kvs):
+    """Pages that the window of every query has passed are gone; the queries and outputs are slices of wider rows."""
+    lens, new, page, window, sinks = [2000], [300], 16, 100, 20
+    k, v, table, n = ref.make(lens, 2, page, seed=12)
+    good = table.clone()
+    for p in range(2, (2000 - 300 - 99) // page):
+        table[0, p] = -1
+    cache = kvs.PagedKV(k, v, table, n)
+    wide = torch.randn(300, 8 * D + 16, device=DEV).to(torch.bfloat16)
+    q = wide[:, 8:8 + 8 * D].view(300, 8, D)
+    ow = torch.zeros(300, 8 * D + 64, dtype=torch.bfloat16, device=DEV)
+    out = ow[:, 64:].view(300, 8, D)
+    st = _status()
+    _, lse = kvs.paged_prompt_attn(q, torch.tensor([0, 300], dtype=torch.int32, device=DEV), cache, window, sinks,
+                                   out=out, dev_status=st)
+    ref.check_prompt(out, lse, q, [0, 300], k, v, good, lens, window, sinks, SC, 2)
+    assert int(st) == 0 and bool((ow[:, :64] == 0).all())
+
+
+def test_prompt_bad_page(kvs):
+    k, v, table, n = ref.make([100], 1, 16, seed=13, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    good = table.clone()
+    table[0, 2] = -1
+    q = torch.randn(100, 2, D, device=DEV).to(torch.bfloat16)
+    st = _status()
+    out, lse = kvs.paged_prompt_attn(q, torch.tensor([0, 100], dtype=torch.int32, device=DEV), cache, dev_status=st)
+    assert int(st) == kvs.KVS_EBOUNDS
+    some = [j for j in range(100) if j // 16 != 2]
+    K, V = ref.tokens(k, good, 0, 100)[some, 0], ref.tokens(v, good, 0, 100)[some, 0]
+    o, ls, _, _, _ = ref.attend(q[99].double(), K, V, SC)
+    assert float((out[99] - o).abs().max()) < 0.03 and float((lse[99] - ls).abs().max()) < 1e-4
+
+
+def test_prompt_stream_and_graph(kvs):
+    k, v, table, n = ref.make([400, 60], 2, 16, seed=15, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(200, 8, D, device=DEV).to(torch.bfloat16)
+    cu = torch.tensor([0, 150, 200], dtype=torch.int32, device=DEV)
+    want, wl = kvs.paged_prompt_attn(q, cu, cache)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got, gl = kvs.paged_prompt_attn(q, cu, cache, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want) and torch.equal(gl, wl)
+    graph = torch.cuda.CUDAGraph()
+    out, lse = torch.zeros_like(want), torch.zeros_like(wl)
+    with torch.cuda.graph(graph):
+        kvs.paged_prompt_attn(q, cu, cache, out=out, lse=lse)
+    for c in ([0, 150, 200], [0, 10, 70], [0, 200, 200]):
+        cu.copy_(torch.tensor(c))
+        q.normal_()
+        graph.replay()
+        ref.check_prompt(out, lse, q, c, k, v, table, [400, 60], 0, 0, SC, 2)
+
+
+def test_decode_and_prompt_agree(kvs):
+    """One new token through either form."""
+    lens = [100, 777, 3, 2050]
+    k, v, table, n = ref.make(lens, 2, 32, seed=17)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(4, 2, 4, D, device=DEV).to(torch.bfloat16)
+    for window, sinks in ((0, 0), (100, 4)):
+        do, dl = kvs.paged_decode_attn(q, cache, window, sinks)
+        po, pl = kvs.paged_prompt_attn(q.view(4, 8, D), torch.arange(5, dtype=torch.int32, device=DEV), cache, window,
+                                       sinks)
+        # the prompt form's two roundings to bf16 (weights, output), each within half a step of values of at most max |V|
+        assert float((do.view(4, 8, D) - po.float()).abs().max()) <= 2 * 2.0 ** -8 * float(v.float().nan_to_num(0).abs().max())
+        assert float((dl.view(4, 8) - pl).abs().max()) < 1e-4
+
+
+# ----------------------------------------------------------------------------- eviction
+
+def _evict_case(kvs, lens, G, page, budget, sinks, recent, seed, mass, pos, seen, layout="head", in_place=True):
+    k, v, table, n = ref.make(lens, G, page, seed=seed, layout=layout)
+    cache = kvs.PagedKV(k, v, table, n)
+    R = len(lens)
+    k0, v0 = k.clone(), v.clone()
+    m0 = mass(R, G, cache.cap)
+    p0 = pos(R, G, cache.cap)
+    m, p = m0.clone(), None if p0 is None else p0.clone()
+    kw = dict(sinks=sinks, recent=recent, pos=p, seen=seen)
+    st = _status()
+    if in_place:
+        src = kvs.paged_evict(cache, m, budget, dev_status=st, **kw)
+        n_out, mo, po = n, m, p
+    else:
+        mo = torch.full_like(m, -1.0)
+        po = None if p is None else torch.full_like(p, -1)
+        n_out = torch.empty_like(n)
+        src = kvs.paged_evict(cache, m, budget, mass_out=mo, pos_out=po, n_out=n_out, dev_status=st, **kw)
+        assert torch.equal(m.nan_to_num(-5), m0.nan_to_num(-5)) and n.tolist() == lens
+    assert int(st) == 0
+    wk, wv = k0.clone(), v0.clone()
+    for r, x in enumerate(lens):
+        assert int(n_out[r]) == min(x, budget)
+        for g in range(G):
+            pr = np.arange(cache.cap) if p0 is None else p0[r, g].cpu().numpy()
+            want = ref.evict(m0[r, g].cpu().numpy(), pr, x, x if seen is None else int(seen[r]), budget, sinks, recent)
+            got = src[r, g].cpu().numpy()
+            assert np.array_equal(got[:len(want)], want) and np.all(got[len(want):] == -1), (r, g)
+            w = torch.from_numpy(want).to(DEV)
+            assert torch.equal(mo[r, g, :len(want)].nan_to_num(-5), m0[r, g, w].nan_to_num(-5))
+            rest = m0[r, g, len(want):] if in_place else torch.full_like(m0[r, g, len(want):], -1.0)
+            assert torch.equal(mo[r, g, len(want):].nan_to_num(-5), rest.nan_to_num(-5)), "entries behind the last"
+            if p0 is not None:
+                assert torch.equal(po[r, g, :len(want)], p0[r, g, w])
+            for j in np.nonzero(want != np.arange(len(want)))[0]:
+                a, b = int(want[j]), int(j)
+                pa, pb = int(table[r, a // page]), int(table[r, b // page])
+                wk[pb, g, b % page], wv[pb, g, b % page] = k0[pa, g, a % page], v0[pa, g, a % page]
+    assert torch.equal(_bits(k), _bits(wk)) and torch.equal(_bits(v), _bits(wv))
+
+
+def _rand(seed, levels=0):
+    def f(R, G, cap):
+        m = torch.rand(R, G, cap, generator=torch.Generator().manual_seed(seed)).to(DEV)
+        return (m * levels).floor() if levels else m
+    return f
+
+
+def _perm(seed):
+    def f(R, G, cap):
+        return torch.argsort(torch.rand(R, G, cap, generator=torch.Generator().manual_seed(seed)), -1).to(
+            torch.int32).to(DEV)
+    return f
+
+
+def _none(*_):
+    return None
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("budget,sinks,recent", [(1, 0, 0), (1, 1, 0), (1, 0, 1), (16, 4, 4), (100, 0, 100), (333, 5, 60),
+                                                 (1024, 4, 300), (2500, 0, 0)])
+def test_evict(kvs, budget, sinks, recent, in_place):
+    _evict_case(kvs, [0, 1, budget, budget + 1, 2 * budget + 3, 2222], 2, 16, budget, sinks, recent, budget,
+                _rand(1), _none, None, in_place=in_place)
+
+
+@pytest.mark.parametrize("levels", [1, 2, 7])
+def test_evict_ties_go_to_the_lower_slot(kvs, levels):
+    _evict_case(kvs, [1500, 64, 65], 2, 64, 64, 3, 9, levels, _rand(2, levels), _none, None, layout="token")
+
+
+def test_evict_places(kvs):
+    """Slots out of order, and a request that has had more tokens than it holds."""
+    lens = [900, 400, 130]
+    seen = torch.tensor([900, 7000, 130], dtype=torch.int32, device=DEV)
+    _evict_case(kvs, lens, 3, 32, 128, 6, 40, 3, _rand(3), _perm(3), seen, layout="both")
+    _evict_case(kvs, lens, 3, 32, 128, 6, 40, 3, _rand(3), _perm(3), None, in_place=False)
+
+
+def test_evict_infinities_nan_and_signed_zero(kvs):
+    def mass(R, G, cap):
+        m = torch.randn(R, G, cap, generator=torch.Generator().manual_seed(4)).to(DEV)
+        pick = torch.randint(0, 6, (R, G, cap), generator=torch.Generator().manual_seed(5)).to(DEV)
+        for i, x in enumerate((float("inf"), float("-inf"), float("nan"), -0.0, 0.0)):
+            m[pick == i] = x
+        return m
+    _evict_case(kvs, [600, 200], 2, 16, 170, 2, 10, 6, mass, _none, None)
+    _evict_case(kvs, [600, 200], 2, 16, 60, 0, 0, 6, mass, _none, None)
+    _evict_case(kvs, [600, 200], 2, 16, 590, 0, 0, 6, mass, _none, None, in_place=False)
+
+
+def test_evict_long_rows(kvs):
+    _evict_case(kvs, [70001, 52000, 9000], 1, 256, 8000, 4, 1000, 7, _rand(7), _none, None)
+
+
+def test_evict_many_rows(kvs):
+    _evict_case(kvs, [40 + i % 30 for i in range(200)], 2, 16, 48, 4, 8, 9, _rand(9), _none, None)
+
+
+def test_evict_bad_page(kvs):
+    """A row whose page id is none does not move; the others do."""
+    k, v, table, n = ref.make([64], 1, 16, seed=20, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    mass = torch.zeros(1, 1, cache.cap, device=DEV)
+    mass[0, 0, 16:64] = 1.0
+    table[0, 3] = -4
+    k0 = k.clone()
+    st = _status()
+    src = kvs.paged_evict(cache, mass, 48, dev_status=st)
+    assert int(st) == kvs.KVS_EBOUNDS
+    assert src[0, 0].tolist() == list(range(48, 64)) + list(range(16, 48))
+    assert torch.equal(_bits(k), _bits(k0))
+
+
+def test_evict_stream_and_graph(kvs):
+    k, v, table, n = ref.make([300, 200], 2, 16, seed=21, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    mass = torch.rand(2, 2, cache.cap, device=DEV)
+    mo, no = torch.zeros_like(mass), torch.zeros_like(n)
+    src = torch.zeros(2, 2, 150, dtype=torch.int32, device=DEV)
+    k0, v0 = k.clone(), v.clone()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a = kvs.paged_evict(cache, mass, 150, mass_out=mo, n_out=no, stream=s).clone()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvs.paged_evict(cache, mass, 150, mass_out=mo, n_out=no, src=src)
+    for i in range(3):
+        k.copy_(k0), v.copy_(v0)
+        graph.replay()
+        for r, x in enumerate([300, 200]):
+            for g in range(2):
+                want = ref.evict(mass[r, g].cpu().numpy(), np.arange(cache.cap), x, x, 150, 0, 0)
+                assert np.array_equal(src[r, g].cpu().numpy(), want)
+                if i == 0:
+                    assert torch.equal(a[r, g], src[r, g])
+        mass.uniform_()
+
+
+# ----------------------------------------------------------------------------- all together
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 3)])
+def test_a_generation_under_a_budget(kvs, window, sinks):
+    """Prompts, then tokens one by one, with the weights added up and the cache cut back to its budget
+    whenever it is 16 tokens over: against a list of tokens for each head that is kept the same way."""
+    R, G, H, page, budget, recent, keep = 3, 2, 4, 16, 96, 24, 2
+    steps, prompt = 40, [150, 30, 97]
+    gen = torch.Generator(device=DEV).manual_seed(33)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device=DEV).to(torch.bfloat16)  # noqa: E731
+    mp = 16
+    pages = R * mp
+    k = torch.full((pages, G, page, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    v = k.clone()
+    table = torch.randperm(pages, generator=gen, device=DEV).to(torch.int32).view(R, mp)
+    n = torch.tensor(prompt, dtype=torch.int32, device=DEV)
+    seen = n.clone()
+    cache = kvs.PagedKV(k, v, table, n)
+    mass = torch.full((R, G, cache.cap), float("nan"), device=DEV)
+    pos = torch.full((R, G, cache.cap), -1, dtype=torch.int32, device=DEV)
+    st = _status()
+
+    cu = torch.tensor([0] + list(np.cumsum(prompt)), dtype=torch.int32, device=DEV)
+    T = int(cu[-1])
+    Kn, Vn, q = rnd(T, G, D), rnd(T, G, D), rnd(T, G * H, D)
+    kvs.paged_append(cache, Kn, Vn, cu, mass=mass, pos=pos, seen=seen, dev_status=st)
+    out, lse = kvs.paged_prompt_attn(q, cu, cache, window, sinks, dev_status=st)
+    ref.check_prompt(out, lse, q, cu.tolist(), k, v, table, prompt, window, sinks, SC, G)
+
+    # the same by lists: (K, V, place) of each head, the weights as the kernels have them
+    K = [[Kn[cu[r]:cu[r + 1], g].double() for g in range(G)] for r in range(R)]
+    V = [[Vn[cu[r]:cu[r + 1], g].double() for g in range(G)] for r in range(R)]
+    at = [[np.arange(prompt[r]) for g in range(G)] for r in range(R)]
+    evictions = 0
+    for step in range(steps):
+        q1, k1, v1 = rnd(R, G, H, D), rnd(R, G, D), rnd(R, G, D)
+        n.add_(1), seen.add_(1)
+        kvs.paged_append(cache, k1, v1, mass=mass, pos=pos, seen=seen, dev_status=st)
+        before = mass.clone()
+        # a window over slots is a window over tokens only until the first eviction
+        w_, s_ = (window, sinks) if evictions == 0 else (0, 0)
+        out, lse = kvs.paged_decode_attn(q1, cache, w_, s_, mass=mass, dev_status=st)
+        lens = n.tolist()
+        for r in range(R):
+            vis = torch.from_numpy(ref.visible(lens[r] - 1, w_, s_)).to(DEV)
+            for g in range(G):
+                K[r][g] = torch.cat([K[r][g], k1[r, g:g + 1].double()])
+                V[r][g] = torch.cat([V[r][g], v1[r, g:g + 1].double()])
+                at[r][g] = np.append(at[r][g], prompt[r] + step)
+                assert K[r][g].shape[0] == lens[r]
+                o, ls, w, e, va = ref.attend(q1[r, g].double(), K[r][g][vis], V[r][g][vis], SC)
+                tol = (4 * e.unsqueeze(-1) + (2 * len(vis) + 64) * ref.U) * va
+                assert bool(((out[r, g] - o).abs() <= tol).all()), (step, r, g)
+                want = before[r, g, vis].double() + w.sum(0)
+                assert float((mass[r, g, vis] - want).abs().max()) < 1e-4
+        if any(x >= budget + 16 for x in lens):
+            evictions += 1
+            m = mass.cpu().numpy()
+            src = kvs.paged_evict(cache, mass, budget, sinks=keep, recent=recent, pos=pos, seen=seen, dev_status=st)
+            for r in range(R):
+                for g in range(G):
+                    s = ref.evict(m[r, g], at[r][g], lens[r], prompt[r] + step + 1, budget, keep, recent)
+                    assert np.array_equal(src[r, g, :len(s)].cpu().numpy(), s)
+                    K[r][g], V[r][g] = K[r][g][torch.from_numpy(s).to(DEV)], V[r][g][torch.from_numpy(s).to(DEV)]
+                    at[r][g] = at[r][g][s]
+                    assert np.array_equal(pos[r, g, :len(s)].cpu().numpy(), at[r][g])
+            assert n.tolist() == [min(x, budget) for x in lens]
+    assert evictions >= 3 and int(st) == 0

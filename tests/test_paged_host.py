@@ -1,0 +1,123 @@
+"""The paged K/V cache's calls refuse bad arguments on the host, before any
+launch (no CUDA call is reached on these paths)."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def kvs():
+    from kv_index_scan_b200 import build
+    build.build()
+    import kv_index_scan_b200
+    return kv_index_scan_b200
+
+
+def _kv(kvs, **change):
+    f = dict(K=4096, V=4096, page_stride=2 * 16 * 128, head_stride=16 * 128, token_stride=128, table=4096, table_ld=8,
+             n=4096, R=2, G=2, D=128, page=16, max_pages=8, num_pages=32)
+    f.update(change)
+    return kvs.PagedKVC(*f.values())
+
+
+BAD_CACHES = [(dict(K=None), 1), (dict(V=None), 1), (dict(table=None), 1), (dict(n=None), 1), (dict(D=64), 2),
+              (dict(R=0), 1), (dict(G=0), 1), (dict(page=8), 2), (dict(page=48), 2), (dict(page=2048), 2),
+              (dict(max_pages=0), 1), (dict(num_pages=0), 1), (dict(table_ld=7), 1), (dict(token_stride=100), 1),
+              (dict(token_stride=132), 1), (dict(head_stride=-128), 1), (dict(page_stride=0), 1), (dict(K=4104), 1),
+              (dict(max_pages=1 << 27, table_ld=1 << 27), 2), (dict(R=1 << 14, G=1 << 12), 2)]
+
+
+@pytest.mark.parametrize("change,status", BAD_CACHES)
+def test_cache_descriptor_checks(kvs, change, status):
+    L, kv = kvs._lib, _kv(kvs, **change)
+    ref = ctypes.pointer(kv)
+    assert L.kvs_paged_append(ref, 4096, 4096, 1 << 20, None, kv.R, None, None, None, None, None) == status
+    d = kvs.PagedDecodeArgsC(ref, 4096, 0, 4, 0, 0, 1.0, 4096, None, None, None)
+    assert L.paged_decode_attn(ctypes.byref(d), 4096, 1 << 40, None, None) == status
+    p = kvs.PagedPromptArgsC(ref, 4096, 1 << 20, 4096, 4, 4, 0, 0, 1.0, 4096, 1 << 20, None)
+    assert L.paged_prompt_attn(ctypes.byref(p), None, None) == status
+    e = kvs.PagedEvictArgsC(ref, 4096, None, None, 8, 0, 0, 4096, None, 4096, 4096)
+    assert L.kvs_paged_evict(ctypes.byref(e), 4096, 1 << 40, None, None) == status
+    assert L.kvs_last_error()
+
+
+def test_null_descriptors(kvs):
+    L = kvs._lib
+    assert L.kvs_paged_append(None, 4096, 4096, 256, None, 2, None, None, None, None, None) == kvs.KVS_EINVAL
+    assert L.paged_decode_attn(None, None, 0, None, None) == kvs.KVS_EINVAL
+    assert L.paged_prompt_attn(None, None, None) == kvs.KVS_EINVAL
+    assert L.kvs_paged_evict(None, None, 0, None, None) == kvs.KVS_EINVAL
+
+
+@pytest.mark.parametrize("args,word", [
+    ((None, 4096, 256, None, 2, None, None, None), b"non-null"),
+    ((4096, 4096, 256, None, 3, None, None, None), b"one token a request"),
+    ((4096, 4096, 256, 4096, -1, None, None, None), b"T=-1"),
+    ((4096, 4096, 128, None, 2, None, None, None), b"new_ld"),
+    ((4096, 4096, 260, None, 2, None, None, None), b"new_ld"),
+    ((4104, 4096, 256, None, 2, None, None, None), b"aligned"),
+    ((4096, 4096, 256, None, 2, None, None, 4096), b"seen"),
+])
+def test_append_checks(kvs, args, word):
+    kv = _kv(kvs)
+    K, V, ld, cu, T, mass, pos, seen = args
+    st = kvs._lib.kvs_paged_append(ctypes.pointer(kv), K, V, ld, cu, T, mass, pos, seen, None, None)
+    assert st == kvs.KVS_EINVAL and word in kvs._lib.kvs_last_error()
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(q=None), 1), (dict(out=None), 1), (dict(q_dtype=2), 1), (dict(H=0), 1), (dict(H=9), 1),
+    (dict(window=-1), 1), (dict(sinks=-1), 1), (dict(mass=4096), 1), (dict(mass_out=4096), 1), (dict(q=4100), 1),
+    (dict(out=4100), 1)])
+def test_decode_checks(kvs, change, status):
+    kv = _kv(kvs)
+    f = dict(kv=ctypes.pointer(kv), q=4096, q_dtype=0, H=4, window=0, sinks=0, scale=1.0, out=4096, lse=None,
+             mass=None, mass_out=None)
+    f.update(change)
+    a = kvs.PagedDecodeArgsC(*f.values())
+    assert kvs._lib.paged_decode_attn(ctypes.byref(a), 4096, 1 << 40, None, None) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(q=None), 1), (dict(out=None), 1), (dict(cu=None), 1), (dict(T=-1), 1), (dict(H=0), 1), (dict(H=9), 1),
+    (dict(window=-1), 1), (dict(sinks=-5), 1), (dict(q_ld=1020), 1), (dict(q_ld=512), 1), (dict(out_ld=1028), 1),
+    (dict(q=4104), 1), (dict(out=4104), 1), (dict(T=1 << 30), 2)])
+def test_prompt_checks(kvs, change, status):
+    kv = _kv(kvs)
+    f = dict(kv=ctypes.pointer(kv), q=4096, q_ld=1024, cu=4096, T=4, H=4, window=0, sinks=0, scale=1.0, out=4096,
+             out_ld=1024, lse=None)
+    f.update(change)
+    a = kvs.PagedPromptArgsC(*f.values())
+    assert kvs._lib.paged_prompt_attn(ctypes.byref(a), None, None) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(mass=None), 1), (dict(mass_out=None), 1), (dict(n_out=None), 1), (dict(src=None), 1), (dict(pos=4096), 1),
+    (dict(pos_out=4096), 1), (dict(budget=0), 1), (dict(sinks=-1), 1), (dict(recent=-1), 1),
+    (dict(sinks=5, recent=4), 1), (dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1), 1)])
+def test_evict_checks(kvs, change, status):
+    kv = _kv(kvs)
+    f = dict(kv=ctypes.pointer(kv), mass=4096, pos=None, seen=None, budget=8, sinks=0, recent=0, mass_out=4096,
+             pos_out=None, n_out=4096, src=4096)
+    f.update(change)
+    a = kvs.PagedEvictArgsC(*f.values())
+    assert kvs._lib.kvs_paged_evict(ctypes.byref(a), 4096, 1 << 40, None, None) == status
+
+
+def test_workspace_checks(kvs):
+    kv = _kv(kvs)
+    a = kvs.PagedEvictArgsC(ctypes.pointer(kv), 4096, None, None, 8, 0, 0, 4096, None, 4096, 4096)
+    need = kvs._lib.kvs_paged_evict_workspace_size(2, 2, 8)
+    assert need > 0
+    assert kvs._lib.kvs_paged_evict(ctypes.byref(a), None, 0, None, None) == kvs.KVS_EWORKSPACE
+    assert kvs._lib.kvs_paged_evict(ctypes.byref(a), 4096, need - 1, None, None) == kvs.KVS_EWORKSPACE
+    assert kvs._lib.kvs_paged_evict(ctypes.byref(a), 4104, 1 << 40, None, None) == kvs.KVS_EINVAL
+
+
+def test_binding_refuses_host_tensors(kvs):
+    pool = torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        kvs.PagedKV(pool, pool, torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="k_pages"):
+        kvs.PagedKV(pool.float(), pool, torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
