@@ -1,54 +1,671 @@
 // paged_decode.cu -- attention of each request's newest token over its paged
-// cache, optionally with the weights added up per token.
-#include "paged_simple.cuh"
+// cache, optionally with every token's softmax weights added up.
+//
+// For (r, g) and query head h: l_j = scale * q_h . K_j over the visible tokens,
+// out = sum_j softmax(l)_j V_j, in base 2 with an online softmax. 512 bytes of
+// K and V are read per token for 4 * 128 * H flops: HBM bounds it.
+//
+//  * The visible tokens of all (r, g) rows are cut into units of 64 and laid
+//    end to end; each block takes an equal run of them, whatever the lengths.
+//    A row that lies inside one run is finished there; of a cut row, each
+//    block leaves its maximum, sum and unnormalised output, and a second
+//    kernel joins them. A run cuts at most the row it begins in and the row it
+//    ends in, so the scratch is two partial rows a block, independent of n.
+//  * One warp loads: a TMA copy per page and pool brings up to 64 tokens of one
+//    head (both 128-byte halves, swizzled) into a ring of three 32 KB stages,
+//    with what the consumers need to know about the unit beside it. Two blocks
+//    share an SM (192 KB in flight).
+//  * Four warps compute, 16 tokens of a unit each: S[tokens][heads] = K q^T and
+//    O^T[dims][heads] += V^T P^T on mma.m16n8k16, tokens as M of the first and
+//    as K of the second, the 8 columns the heads. bf16 queries are exact; f32
+//    queries and the weights are split in three bf16 parts (24 bits). Each
+//    16-token product is summed in the tensor core and added to the running
+//    output in f32 with the rescaling as one fma: the tensor core truncates
+//    its sums, and over thousands of tokens that would show.
+//  * V rows that are masked or were not loaded are cleared in the registers:
+//    whatever lies there (NaN too) must not meet a weight of zero.
+//  * With weights wanted, the logits go to scratch (4 H bytes a token beside
+//    the 512 read) and the join turns them into weights, once the row's
+//    log-sum-exp is known.
+#include <cuda_bf16.h>
+
+#include "async.cuh"
 
 namespace kvs {
 
 namespace {
 
-__global__ void __launch_bounds__(kSimpleThreads) paged_decode_simple_kernel(PagedView kv, kvs_paged_decode_args a,
-                                                                             int32_t* dev_status) {
+constexpr int kUnit = 64;
+constexpr int kStages = 3;
+constexpr int kConsumers = 4;  // warps, 16 tokens of a unit each
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kBlocksPerSM = 2;
+constexpr int kPoolBytes = kUnit * kD * 2;     // K or V of a unit
+constexpr int kStageBytes = 2 * kPoolBytes;
+constexpr int kMinUnits = 2;                   // units a block takes at least
+constexpr int kPartRow = kD + 4;               // maximum, sum, -, -, output
+constexpr int kPartSlots = 2;
+
+// flags of a unit, beside the bits of its four 16-token groups that were loaded
+constexpr int kFirst = 16, kLast = 32, kSlotShift = 6;  // slot 0: complete row, 1 + s: partial slot s
+
+struct UnitInfo {
+  int row;   // r * G + g
+  int tok;   // first token
+  int n;
+  int flags;
+};
+
+struct DecodeSmem {
+  alignas(1024) unsigned char ring[kStages][kStageBytes];
+  float merge[kConsumers - 1][8][kD];
+  float ml[kConsumers - 1][8][2];
+  UnitInfo info[kStages];
+  uint64_t full[kStages], empty[kStages];
+  int abort_flag;
+};
+
+struct DecodeParams {
+  PagedView kv;
+  const void* q;
+  int H, window, sinks;
+  float scale_log2;
+  float* out;
+  float* lse;
+  const float* mass;
+  float* mass_out;
+  float* part;     // [blocks][kPartSlots][H][kPartRow]
+  float* lse2;     // [R*G][H], base 2, of rows that one block finished (weights only)
+  float* logits;   // [R*G][cap][hp], base 2 (weights only)
+  int hp;          // H rounded up to an even number
+  int blocks;
+  int32_t* dev_status;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+      "%2, %3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+// x and y as bf16 in one register, and what the rounding left of them
+__device__ __forceinline__ uint32_t take_bf16(float& x, float& y) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+  const uint32_t b = *reinterpret_cast<const uint32_t*>(&v);
+  x -= __uint_as_float(b << 16);
+  y -= __uint_as_float(b & 0xFFFF0000u);
+  return b;
+}
+
+// Blocks that share U units (every kernel computes the same), and the first
+// unit of block b.
+__device__ __forceinline__ int sharing(int64_t U, int blocks) {
+  const int64_t most = (U + kMinUnits - 1) / kMinUnits;
+  return most < blocks ? static_cast<int>(most) : blocks;
+}
+__device__ __forceinline__ int64_t first_unit(int64_t U, int b, int nb) { return U * b / nb; }
+__device__ __forceinline__ int block_of_unit(int64_t U, int64_t x, int nb) {
+  return static_cast<int>(((x + 1) * nb - 1) / U);
+}
+
+// Sum over the block of each thread's v, and the sum of the threads before it.
+template <int kT>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t& total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t inc = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+    if (lane >= d) inc += y;
+  }
+  if (lane == 31) part[warp] = inc;
+  __syncthreads();
+  int64_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kT / 32; ++w) {
+    if (w < warp) before += part[w];
+    total += part[w];
+  }
+  return before + inc - v;
+}
+
+template <bool kF32Q, bool kWeights>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(const DecodeParams p,
+                                                                              const __grid_constant__ CUtensorMap mapK,
+                                                                              const __grid_constant__ CUtensorMap mapV) {
+  extern __shared__ __align__(1024) unsigned char decode_smem[];
+  DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>(decode_smem);
+  __shared__ int64_t scan_part[kThreads / 32];
+  __shared__ int64_t s_base;
+  __shared__ int s_r;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const PagedView& kv = p.kv;
+  const int G = kv.G;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], kConsumers);
+    }
+    sm.abort_flag = 0;
+    mbar_init_fence();
+    tma_prefetch_map(&mapK);
+    tma_prefetch_map(&mapV);
+  }
   pdl_wait();
-  __shared__ SimpleSmem s;
-  const int u = blockIdx.x, r = u / kv.G, g = u % kv.G, tid = threadIdx.x;
-  const int n = kv.length(r, dev_status);
-  for (int h = 0; h < a.H; ++h) {
-    const size_t at = (static_cast<size_t>(u) * a.H + h) * kD + tid;
-    const float q = a.q_dtype == KVS_BF16 ? bf16_bits_to_float(static_cast<const uint16_t*>(a.q)[at])
-                                          : static_cast<const float*>(a.q)[at];
-    __syncthreads();
-    s.q[tid] = q * a.scale;
-    __syncthreads();
-    float lse;
-    a.out[at] = simple_attend(kv, r, g, n - 1, a.window, a.sinks, s, lse, dev_status);
-    if (a.lse && tid == 0) a.lse[static_cast<size_t>(u) * a.H + h] = lse;
-    if (!a.mass) continue;
-    for (int j = tid; j < n; j += kSimpleThreads) {
-      if (a.window && j >= a.sinks && j < n - a.window) continue;
-      const size_t m = static_cast<size_t>(u) * kv.cap() + j;
-      const int id = kv.page_of(r, j, dev_status);
-      float w = 0.f;
-      if (id >= 0) {
-        float acc = 0.f;
-        for (int d = 0; d < kD; ++d) acc = fmaf(s.q[d], bf16_bits_to_float(kv.K[kv.row(id, g, j) + d]), acc);
-        w = expf(acc - lse);
+  pdl_trigger();
+
+  // this block's run of units, and the request it begins in
+  const int per = (kv.R + kThreads - 1) / kThreads;
+  const int r_lo = min(kv.R, tid * per), r_hi = min(kv.R, r_lo + per);
+  int64_t mine = 0;
+  for (int r = r_lo; r < r_hi; ++r)
+    mine += VisibleTiles<kUnit>(kv.length(r, p.dev_status), p.window, p.sinks).count;
+  int64_t U;
+  int64_t before = block_scan<kThreads>(mine, scan_part, U) * G;
+  U *= G;
+  const int nb = sharing(U, p.blocks);
+  if (static_cast<int>(blockIdx.x) >= nb) return;
+  const int64_t u0 = first_unit(U, blockIdx.x, nb), u1 = first_unit(U, blockIdx.x + 1, nb);
+  if (u0 >= before && u0 < before + mine * G) {
+    int r = r_lo;
+    for (;; ++r) {
+      const int64_t c = static_cast<int64_t>(VisibleTiles<kUnit>(kv.length(r, nullptr), p.window, p.sinks).count) * G;
+      if (u0 < before + c) break;
+      before += c;
+    }
+    s_r = r;
+    s_base = before;
+  }
+  __syncthreads();
+  const int units = static_cast<int>(u1 - u0);
+
+  auto fail = [&] {
+    set_status(p.dev_status, KVS_ETIMEOUT);
+    atomicExch(&sm.abort_flag, 1);
+  };
+  auto aborted = [&] { return *reinterpret_cast<volatile int*>(&sm.abort_flag) != 0; };
+
+  if (warp == kConsumers) {
+    // ---------------- loads ----------------
+    const int rows = min(1 << kv.shift, kUnit), copies = 2 * (kUnit / rows);
+    const bool isv = lane & 1;
+    const int sub = lane >> 1;  // this lane's page within the unit
+    int r = s_r;
+    VisibleTiles<kUnit> vt(kv.length(r, nullptr), p.window, p.sinks);
+    int k = static_cast<int>((u0 - s_base) % vt.count), g = static_cast<int>((u0 - s_base) / vt.count);
+    const int k_start = k;
+    UnitInfo next;
+    int next_id;
+    // the unit at (r, g, k), its flags and this lane's page
+    auto look = [&](int i) {
+      next.row = r * G + g;
+      next.tok = vt.tile(k) * kUnit;
+      next.n = vt.end;
+      next.flags = 0;
+      if (i == 0 || k == 0) next.flags |= kFirst;
+      if (i == units - 1 || k == vt.count - 1) {
+        next.flags |= kLast;
+        const bool began_before = k_start > 0 && k == k_start + i;  // still the row that the run begins in
+        const bool goes_on = k < vt.count - 1;
+        next.flags |= (began_before ? 1 : (goes_on ? 2 : 0)) << kSlotShift;
       }
-      a.mass_out[m] = (h == 0 ? a.mass[m] : a.mass_out[m]) + w;
+      const int t = next.tok + sub * rows;
+      next_id = -1;
+      if (lane < copies && t < vt.end && (t < p.sinks || t + rows > vt.lo)) next_id = kv.page_of(r, t, p.dev_status);
+    };
+    look(0);
+    int issued = 0;
+    for (int i = 0; i < units; ++i) {
+      const int st = i % kStages;
+      const UnitInfo info = next;
+      const int id = next_id;
+      if (i + 1 < units) {
+        if (++k == vt.count) {
+          k = 0;
+          if (++g == G) {
+            g = 0;
+            do {
+              ++r;
+              vt = VisibleTiles<kUnit>(kv.length(r, nullptr), p.window, p.sinks);
+            } while (vt.count == 0);
+          }
+        }
+        look(i + 1);
+      }
+      const unsigned have = __ballot_sync(0xFFFFFFFFu, id >= 0);
+      int ok = 1;
+      if (lane == 0) {
+        if (i >= kStages && !mbar_wait(&sm.empty[st], (i / kStages - 1) & 1)) {
+          fail();
+          ok = 0;
+        }
+        if (aborted()) ok = 0;
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (!ok) break;
+      if (lane == 0) {
+        int groups = 0;  // 16-token groups that are there
+        for (int e = 0; e < 4; ++e)
+          if (have >> (2 * (16 * e / rows)) & 1u) groups |= 1 << e;
+        sm.info[st] = {info.row, info.tok, info.n, info.flags | groups};
+        if (have) mbar_expect(&sm.full[st], __popc(have) * rows * kD * 2);
+        else mbar_arrive(&sm.full[st]);
+      }
+      __syncwarp();
+      if (id >= 0) {
+        const int in_page = (info.tok + sub * rows) & ((1 << kv.shift) - 1);
+        tma_page_rows(sm_addr(sm.ring[st]) + (isv ? kPoolBytes : 0) + sub * rows * kD * 2, isv ? &mapV : &mapK, in_page,
+                      0, info.row % G, id, &sm.full[st]);
+      }
+      ++issued;
+    }
+    // no copy may be in flight when the block ends
+    if (lane == 0)
+      for (int i = max(0, issued - kStages); i < issued; ++i) mbar_wait(&sm.full[i % kStages], (i / kStages) & 1);
+    return;
+  }
+
+  // ---------------- arithmetic ----------------
+  const float ninf = -__int_as_float(0x7f800000);
+  const int gq = lane >> 2, tq = lane & 3;  // fragment row and column pair
+  const int hA = 2 * tq, hB = hA + 1;       // this lane's heads
+  const int H = p.H;
+  const int rows = min(1 << kv.shift, kUnit);
+  const uint32_t half = rows * kD;  // bytes from a row's first half to its second
+  const uint32_t grp = (16 * warp / rows) * rows * kD * 2 + (16 * warp % rows) * kD;
+  // ldmatrix rows of this lane: K (tokens as rows) and V (tokens as columns)
+  const int krow = lane & 15, kc = lane >> 4;
+  const int vrow = (lane & 7) + 8 * (lane >> 4), vc = (lane >> 3) & 1;
+  const uint32_t koff = grp + krow * kD, voff = kPoolBytes + grp + vrow * kD;
+  constexpr int kQ = kF32Q ? 3 : 1;
+  uint32_t qf[kQ][8][2];
+  float o[8][4];
+  float mA = ninf, mB = ninf, lA = 0.f, lB = 0.f;
+
+  for (int i = 0; i < units; ++i) {
+    const int st = i % kStages;
+    int ok = 1;
+    if (lane == 0 && !mbar_wait(&sm.full[st], (i / kStages) & 1)) {
+      fail();
+      ok = 0;
+    }
+    // a stage that one warp has seen full stays so until all have released it:
+    // the four warps stop at the same unit, and none is left at a barrier
+    if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+    const UnitInfo info = sm.info[st];
+    if (info.flags & kFirst) {
+      // a new row: its queries, head = fragment column gq
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const size_t at = (static_cast<size_t>(info.row) * H + min(gq, H - 1)) * kD + 16 * ks + 8 * e + 2 * tq;
+          if constexpr (kF32Q) {
+            float2 v = *reinterpret_cast<const float2*>(static_cast<const float*>(p.q) + at);
+#pragma unroll
+            for (int s = 0; s < 3; ++s) qf[s][ks][e] = take_bf16(v.x, v.y);
+          } else {
+            qf[0][ks][e] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) + at);
+          }
+        }
+#pragma unroll
+      for (int d = 0; d < 8; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+      mA = mB = ninf;
+      lA = lB = 0.f;
+    }
+    const int t0 = info.tok + 16 * warp;
+    const int lo = p.window && info.n > p.window ? info.n - p.window : 0;
+    const bool there = info.flags >> warp & 1;
+    auto sees = [&](int t) { return there && t < info.n && (t >= lo || t < p.sinks); };
+    const bool v0 = sees(t0 + gq), v8 = sees(t0 + gq + 8);
+    const bool any = __any_sync(0xFFFFFFFFu, v0 || v8);
+    const bool all = __all_sync(0xFFFFFFFFu, v0 && v8);
+    float s4[4] = {ninf, ninf, ninf, ninf};
+    if (any) {
+      const uint32_t base = sm_addr(sm.ring[st]);
+      // S[tokens][heads]
+      // (the lower parts of f32 queries summed apart: fewer truncations at full size)
+      float sc[4] = {0.f, 0.f, 0.f, 0.f}, sl[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        uint32_t a[4];
+        ldsm4(base + koff + (ks >> 2) * half + (((2 * (ks & 3) + kc) ^ (krow & 7)) << 4), a);
+        mma16816(sc, a, qf[0][ks][0], qf[0][ks][1]);
+#pragma unroll
+        for (int s = kQ - 1; s > 0; --s) mma16816(sl, a, qf[s][ks][0], qf[s][ks][1]);
+      }
+      if constexpr (kF32Q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[e] += sl[e];
+      s4[0] = v0 ? sc[0] * p.scale_log2 : ninf;
+      s4[1] = v0 ? sc[1] * p.scale_log2 : ninf;
+      s4[2] = v8 ? sc[2] * p.scale_log2 : ninf;
+      s4[3] = v8 ? sc[3] * p.scale_log2 : ninf;
+      float xA = fmaxf(s4[0], s4[2]), xB = fmaxf(s4[1], s4[3]);
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        xA = fmaxf(xA, __shfl_xor_sync(0xFFFFFFFFu, xA, d));
+        xB = fmaxf(xB, __shfl_xor_sync(0xFFFFFFFFu, xB, d));
+      }
+      const float nA = fmaxf(mA, xA), nB = fmaxf(mB, xB);
+      // a head whose logits are all -inf keeps its maximum there: reference 0
+      const float fA = nA == ninf ? 0.f : nA, fB = nB == ninf ? 0.f : nB;
+      const float alA = exp2f(mA - fA), alB = exp2f(mB - fB);
+      float w4[4] = {exp2f(s4[0] - fA), exp2f(s4[1] - fB), exp2f(s4[2] - fA), exp2f(s4[3] - fB)};
+      lA = lA * alA + (w4[0] + w4[2]);
+      lB = lB * alB + (w4[1] + w4[3]);
+      mA = nA;
+      mB = nB;
+      // P^T, in three parts
+      uint32_t b[3][2];
+#pragma unroll
+      for (int s = 0; s < 3; ++s) {
+        b[s][0] = transpose8x8(take_bf16(w4[0], w4[1]));
+        b[s][1] = transpose8x8(take_bf16(w4[2], w4[3]));
+      }
+      // V rows of this lane's fragment columns, cleared where they are not seen
+      const uint32_t k0 = (sees(t0 + 2 * tq) ? 0xFFFFu : 0u) | (sees(t0 + 2 * tq + 1) ? 0xFFFF0000u : 0u);
+      const uint32_t k8 = (sees(t0 + 2 * tq + 8) ? 0xFFFFu : 0u) | (sees(t0 + 2 * tq + 9) ? 0xFFFF0000u : 0u);
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        uint32_t a[4];
+        ldsm4_trans(base + voff + (mt >> 2) * half + (((2 * (mt & 3) + vc) ^ (vrow & 7)) << 4), a);
+        if (!all) {
+          a[0] &= k0;
+          a[1] &= k0;
+          a[2] &= k8;
+          a[3] &= k8;
+        }
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 2; s >= 0; --s) mma16816(c, a, b[s][0], b[s][1]);
+        o[mt][0] = fmaf(o[mt][0], alA, c[0]);
+        o[mt][1] = fmaf(o[mt][1], alB, c[1]);
+        o[mt][2] = fmaf(o[mt][2], alA, c[2]);
+        o[mt][3] = fmaf(o[mt][3], alB, c[3]);
+      }
+    }
+    if constexpr (kWeights) {
+      if (hA < p.hp) {
+        float* l = p.logits + (static_cast<size_t>(info.row) * kv.cap() + t0 + gq) * p.hp + hA;
+        if (t0 + gq < info.n) *reinterpret_cast<float2*>(l) = make_float2(s4[0], s4[1]);
+        if (t0 + gq + 8 < info.n) *reinterpret_cast<float2*>(l + 8 * p.hp) = make_float2(s4[2], s4[3]);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.empty[st]);
+
+    if (info.flags & kLast) {
+      // the row ends here, or this block's part of it: the warps' parts into warp 0's
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        lA += __shfl_xor_sync(0xFFFFFFFFu, lA, d);
+        lB += __shfl_xor_sync(0xFFFFFFFFu, lB, d);
+      }
+      if (warp > 0) {
+        float(&mo)[8][kD] = sm.merge[warp - 1];
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          mo[hA][16 * mt + gq] = o[mt][0];
+          mo[hB][16 * mt + gq] = o[mt][1];
+          mo[hA][16 * mt + gq + 8] = o[mt][2];
+          mo[hB][16 * mt + gq + 8] = o[mt][3];
+        }
+        if (gq == 0) {
+          sm.ml[warp - 1][hA][0] = mA;
+          sm.ml[warp - 1][hA][1] = lA;
+          sm.ml[warp - 1][hB][0] = mB;
+          sm.ml[warp - 1][hB][1] = lB;
+        }
+      }
+      asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kConsumers) : "memory");
+      if (warp == 0) {
+        float MA = mA, MB = mB;
+#pragma unroll
+        for (int w = 0; w < kConsumers - 1; ++w) {
+          MA = fmaxf(MA, sm.ml[w][hA][0]);
+          MB = fmaxf(MB, sm.ml[w][hB][0]);
+        }
+        const float fA = MA == ninf ? 0.f : MA, fB = MB == ninf ? 0.f : MB;
+        const float sA = exp2f(mA - fA), sB = exp2f(mB - fB);
+        lA *= sA;
+        lB *= sB;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          o[mt][0] *= sA;
+          o[mt][1] *= sB;
+          o[mt][2] *= sA;
+          o[mt][3] *= sB;
+        }
+#pragma unroll
+        for (int w = 0; w < kConsumers - 1; ++w) {
+          const float cA = exp2f(sm.ml[w][hA][0] - fA), cB = exp2f(sm.ml[w][hB][0] - fB);
+          lA = fmaf(sm.ml[w][hA][1], cA, lA);
+          lB = fmaf(sm.ml[w][hB][1], cB, lB);
+          float(&mo)[8][kD] = sm.merge[w];
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) {
+            o[mt][0] = fmaf(mo[hA][16 * mt + gq], cA, o[mt][0]);
+            o[mt][1] = fmaf(mo[hB][16 * mt + gq], cB, o[mt][1]);
+            o[mt][2] = fmaf(mo[hA][16 * mt + gq + 8], cA, o[mt][2]);
+            o[mt][3] = fmaf(mo[hB][16 * mt + gq + 8], cB, o[mt][3]);
+          }
+        }
+        const int slot = info.flags >> kSlotShift;
+        float *dA, *dB;
+        float iA = 1.f, iB = 1.f;
+        if (slot == 0) {
+          dA = p.out + (static_cast<size_t>(info.row) * H + hA) * kD;
+          dB = dA + kD;
+          iA = lA > 0.f ? 1.f / lA : (lA == 0.f ? 0.f : lA);  // nothing seen: 0; NaN stays
+          iB = lB > 0.f ? 1.f / lB : (lB == 0.f ? 0.f : lB);
+          if (gq == 0) {
+            const float zA = lA == 0.f ? ninf : MA + log2f(lA), zB = lB == 0.f ? ninf : MB + log2f(lB);
+            const size_t at = static_cast<size_t>(info.row) * H + hA;
+            if (p.lse && hA < H) p.lse[at] = zA * 0.6931471805599453f;
+            if (p.lse && hB < H) p.lse[at + 1] = zB * 0.6931471805599453f;
+            if (kWeights && hA < H) p.lse2[at] = zA;
+            if (kWeights && hB < H) p.lse2[at + 1] = zB;
+          }
+        } else {
+          float* pp = p.part + ((static_cast<size_t>(blockIdx.x) * kPartSlots + slot - 1) * H + hA) * kPartRow;
+          if (gq == 0 && hA < H) pp[0] = MA, pp[1] = lA;
+          if (gq == 0 && hB < H) pp[kPartRow] = MB, pp[kPartRow + 1] = lB;
+          dA = pp + 4;
+          dB = dA + kPartRow;
+        }
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          if (hA < H) {
+            dA[16 * mt + gq] = o[mt][0] * iA;
+            dA[16 * mt + gq + 8] = o[mt][2] * iA;
+          }
+          if (hB < H) {
+            dB[16 * mt + gq] = o[mt][1] * iB;
+            dB[16 * mt + gq + 8] = o[mt][3] * iB;
+          }
+        }
+      }
+      asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kConsumers) : "memory");
     }
   }
 }
 
-}  // namespace
+constexpr int kJoinThreads = 256;
+constexpr int kJoinTokens = 2048;  // tokens of a row that one block turns into weights
 
-size_t paged_decode_ws_bytes(int R, int G, int H, int weight_cap) {
-  (void)R, (void)G, (void)H, (void)weight_cap;
-  return 0;
+// Row u's parts joined (block x = 0 of the row), and its weights (every block).
+template <bool kWeights>
+__global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const DecodeParams p, int chunks) {
+  __shared__ int64_t scan_part[kJoinThreads / 32];
+  __shared__ float s_lse2[8];
+  pdl_wait();
+  const float ninf = -__int_as_float(0x7f800000);
+  const PagedView& kv = p.kv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int u = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
+  const int r = u / kv.G, g = u % kv.G, H = p.H;
+  const VisibleTiles<kUnit> vt(kv.length(r, nullptr), p.window, p.sinks);
+  if (chunk > 0 && static_cast<int64_t>(chunk) * (kJoinTokens / kUnit) >= vt.count) return;
+  int64_t all = 0, before = 0;
+  for (int x = tid; x < kv.R; x += kJoinThreads) {
+    const int c = VisibleTiles<kUnit>(kv.length(x, nullptr), p.window, p.sinks).count;
+    all += c;
+    if (x < r) before += c;
+  }
+  int64_t U, base;
+  block_scan<kJoinThreads>(all, scan_part, U);
+  __syncthreads();
+  block_scan<kJoinThreads>(before, scan_part, base);
+  U *= kv.G;
+  base = base * kv.G + static_cast<int64_t>(g) * vt.count;
+  int b0 = 0, b1 = 0;
+  if (vt.count) {
+    const int nb = sharing(U, p.blocks);
+    b0 = block_of_unit(U, base, nb);
+    b1 = block_of_unit(U, base + vt.count - 1, nb);
+  }
+  if (vt.count == 0) {
+    for (int e = tid; e < H * kD; e += kJoinThreads) p.out[static_cast<size_t>(u) * H * kD + e] = 0.f;
+    if (p.lse && tid < H) p.lse[static_cast<size_t>(u) * H + tid] = ninf;
+    return;
+  }
+  if (b0 == b1) {
+    if (!kWeights) return;
+    if (tid < H) s_lse2[tid] = p.lse2[static_cast<size_t>(u) * H + tid];
+  } else {
+    // part x: block b0 + x, in its second slot where the row begins
+    const int parts = b1 - b0 + 1;
+    auto part = [&](int x, int h) {
+      return p.part + ((static_cast<size_t>(b0 + x) * kPartSlots + (x == 0 ? 1 : 0)) * H + h) * kPartRow;
+    };
+    if (warp < H) {
+      const int h = warp;
+      float M = ninf;
+      for (int x = lane; x < parts; x += 32) M = fmaxf(M, part(x, h)[0]);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+      const float f = M == ninf ? 0.f : M;
+      float L = 0.f;
+      for (int x = lane; x < parts; x += 32) L = fmaf(part(x, h)[1], exp2f(part(x, h)[0] - f), L);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, d);
+      const float z = L == 0.f ? ninf : M + log2f(L);
+      if (lane == 0) s_lse2[h] = z;
+      if (chunk == 0) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int x = 0; x < parts; ++x) {
+          const float* pp = part(x, h);
+          const float c = exp2f(pp[0] - f);
+          const float4 v = *reinterpret_cast<const float4*>(pp + 4 + 4 * lane);
+          acc.x = fmaf(c, v.x, acc.x);
+          acc.y = fmaf(c, v.y, acc.y);
+          acc.z = fmaf(c, v.z, acc.z);
+          acc.w = fmaf(c, v.w, acc.w);
+        }
+        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+        *reinterpret_cast<float4*>(p.out + (static_cast<size_t>(u) * H + h) * kD + 4 * lane) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (p.lse && lane == 0) p.lse[static_cast<size_t>(u) * H + h] = z * 0.6931471805599453f;
+      }
+    }
+  }
+  if constexpr (kWeights) {
+    __syncthreads();
+    const size_t row = static_cast<size_t>(u) * kv.cap();
+    for (int e = tid; e < kJoinTokens; e += kJoinThreads) {
+      const int k = chunk * (kJoinTokens / kUnit) + e / kUnit;
+      if (k >= vt.count) break;
+      const int t = vt.tile(k) * kUnit + e % kUnit;
+      if (t >= vt.end || (t < vt.lo && t >= p.sinks)) continue;
+      const float* l = p.logits + (row + t) * p.hp;
+      float w = 0.f;
+      for (int h = 0; h < H; ++h) {
+        const float z = s_lse2[h];
+        w += z == ninf ? 0.f : exp2f(l[h] - z);
+      }
+      p.mass_out[row + t] = p.mass[row + t] + w;
+    }
+  }
 }
 
+int decode_blocks() { return kBlocksPerSM * sm_count(); }
+
+size_t carve(DecodeParams* p, void* ws, int R, int G, int H, int weight_cap) {
+  WsCarver c(ws);
+  const int hp = (H + 1) / 2 * 2;
+  float* part = c.take<float>(static_cast<size_t>(decode_blocks()) * kPartSlots * H * kPartRow);
+  float* lse2 = weight_cap ? c.take<float>(static_cast<size_t>(R) * G * H) : nullptr;
+  float* logits = weight_cap ? c.take<float>(static_cast<size_t>(R) * G * weight_cap * hp) : nullptr;
+  if (p) {
+    p->part = part;
+    p->lse2 = lse2;
+    p->logits = logits;
+    p->hp = hp;
+  }
+  return align_up(c.used, 16);
+}
+
+template <bool kF32Q, bool kWeights>
+void launch(const DecodeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+  cudaFuncSetAttribute(paged_decode_kernel<kF32Q, kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       static_cast<int>(sizeof(DecodeSmem)));
+  launch_chained(paged_decode_kernel<kF32Q, kWeights>, dim3(p.blocks), dim3(kThreads), sizeof(DecodeSmem), s, p, mk,
+                 mv);
+  const int chunks = kWeights ? (p.kv.max_pages * (1 << p.kv.shift) + kJoinTokens - 1) / kJoinTokens : 1;
+  launch_chained(paged_decode_join_kernel<kWeights>, dim3(p.kv.R * p.kv.G * chunks), dim3(kJoinThreads), 0, s, p,
+                 chunks);
+}
+
+}  // namespace
+
+size_t paged_decode_ws_bytes(int R, int G, int H, int weight_cap) { return carve(nullptr, nullptr, R, G, H, weight_cap); }
+
 kvs_status paged_decode_launch(const kvs_paged_decode_args* a, void* ws, int32_t* dev_status, cudaStream_t s) {
-  (void)ws;
-  const PagedView kv = paged_view(a->kv);
-  launch_chained(paged_decode_simple_kernel, dim3(kv.R * kv.G), dim3(kSimpleThreads), 0, s, kv, *a, dev_status);
+  DecodeParams p{};
+  p.kv = paged_view(a->kv);
+  p.q = a->q;
+  p.H = a->H;
+  p.window = a->window;
+  p.sinks = a->sinks;
+  p.scale_log2 = a->scale * 1.4426950408889634f;
+  p.out = a->out;
+  p.lse = a->lse;
+  p.mass = a->mass;
+  p.mass_out = a->mass_out;
+  p.blocks = decode_blocks();
+  p.dev_status = dev_status;
+  carve(&p, ws, p.kv.R, p.kv.G, p.H, a->mass ? a->kv->max_pages * a->kv->page : 0);
+  const int rows = a->kv->page < kUnit ? a->kv->page : kUnit;
+  CUtensorMap mk, mv;
+  kvs_status st = paged_tensor_map(&mk, a->kv->K, p.kv, rows, 2, "paged_decode_attn");
+  if (st == KVS_OK) st = paged_tensor_map(&mv, a->kv->V, p.kv, rows, 2, "paged_decode_attn");
+  if (st != KVS_OK) return st;
+  const bool f32 = a->q_dtype == KVS_F32;
+  if (f32 && a->mass) launch<true, true>(p, mk, mv, s);
+  else if (f32) launch<true, false>(p, mk, mv, s);
+  else if (a->mass) launch<false, true>(p, mk, mv, s);
+  else launch<false, false>(p, mk, mv, s);
   return check_launch("paged_decode_attn");
 }
 
