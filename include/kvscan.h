@@ -487,7 +487,7 @@ KVS_API kvs_status kvs_paged_append(const kvs_paged_kv* kv, const uint16_t* Knew
  * out = sum_j softmax(l)_j V_j and lse = log sum_j exp(l_j). A request with no
  * visible token gets out = 0 and lse = -inf.
  *   q f32 or bf16 [R][G][H][D]; out f32 [R][G][H][D]; lse (nullable) f32
- *   [R][G][H]. H in 1..8.
+ *   [R][G][H]. H in 1..8; scale finite and not 0 (in both attentions).
  * mass, mass_out (both or neither) f32 [R][G][max_pages * page]: for every
  * visible token mass_out[j] = mass[j] + sum_h softmax(l)_hj; the other entries
  * of mass_out stay as they are. mass_out may be mass itself, or not overlap it.
@@ -519,8 +519,9 @@ KVS_API size_t kvs_paged_decode_workspace_size(int32_t R, int32_t G, int32_t H, 
  *   q bf16 [T][G*H][D] (query heads g*H .. g*H + H-1 share KV head g), tokens
  *   q_ld elements apart; out bf16 likewise with out_ld; lse (nullable) f32
  *   [T][G*H]. H in 1..8; q_ld, out_ld multiples of 8, q and out 16-byte
- *   aligned. Packed rows from cu[R] on are neither read nor written; a query that sees
- *   nothing (p < 0) gets out = 0 and lse = -inf.
+ *   aligned. Packed rows from cu[R] on are neither read nor written; a query
+ *   that sees nothing (p < 0) gets out = 0 and lse = -inf. Entries of cu
+ *   outside 0 .. T are clamped (KVS_EBOUNDS).
  * The softmax and all sums are f32; the weights are rounded to bf16 for the
  * product with V, and out once at the end. A cached V row that is not finite
  * makes the outputs of queries not finite that see it, and may those of

@@ -1,6 +1,8 @@
 // paged_api.cu -- the extern "C" boundary of the paged K/V cache: argument
 // checks on the host (nothing is launched or written when a check fails) and
 // the launches, all on the caller's stream.
+#include <cmath>
+
 #include "paged.cuh"
 
 namespace kvs {
@@ -51,7 +53,9 @@ kvs_status check_paged(const char* who, const kvs_paged_kv* kv) {
   return KVS_OK;
 }
 
-kvs_status check_window(const char* who, int window, int sinks) {
+kvs_status check_mask(const char* who, int window, int sinks, float scale) {
+  KVS_REQUIRE(std::isfinite(scale) && scale != 0.f, KVS_EINVAL, "%s: scale=%g must be finite and not 0", who,
+              static_cast<double>(scale));
   KVS_REQUIRE(window >= 0 && sinks >= 0, KVS_EINVAL, "%s: window=%d sinks=%d must not be negative", who, window,
               sinks);
   return KVS_OK;
@@ -93,7 +97,7 @@ kvs_status paged_decode_attn(const kvs_paged_decode_args* a, void* ws, size_t ws
                              void* stream) {
   KVS_REQUIRE(a != nullptr, KVS_EINVAL, "paged_decode_attn: args is null");
   KVS_PROPAGATE(check_paged("paged_decode_attn", a->kv));
-  KVS_PROPAGATE(check_window("paged_decode_attn", a->window, a->sinks));
+  KVS_PROPAGATE(check_mask("paged_decode_attn", a->window, a->sinks, a->scale));
   KVS_REQUIRE(a->q && a->out, KVS_EINVAL, "paged_decode_attn: q and out must be non-null");
   KVS_REQUIRE(a->q_dtype == KVS_F32 || a->q_dtype == KVS_BF16, KVS_EINVAL, "paged_decode_attn: q_dtype=%d", a->q_dtype);
   KVS_REQUIRE(a->H >= 1 && a->H <= 8, KVS_EINVAL, "paged_decode_attn: H=%d query heads per KV head (1..8)", a->H);
@@ -112,7 +116,7 @@ kvs_status paged_decode_attn(const kvs_paged_decode_args* a, void* ws, size_t ws
 kvs_status paged_prompt_attn(const kvs_paged_prompt_args* a, int32_t* dev_status, void* stream) {
   KVS_REQUIRE(a != nullptr, KVS_EINVAL, "paged_prompt_attn: args is null");
   KVS_PROPAGATE(check_paged("paged_prompt_attn", a->kv));
-  KVS_PROPAGATE(check_window("paged_prompt_attn", a->window, a->sinks));
+  KVS_PROPAGATE(check_mask("paged_prompt_attn", a->window, a->sinks, a->scale));
   KVS_REQUIRE(a->T >= 0, KVS_EINVAL, "paged_prompt_attn: T=%d", a->T);
   KVS_REQUIRE(a->H >= 1 && a->H <= 8, KVS_EINVAL, "paged_prompt_attn: H=%d query heads per KV head (1..8)", a->H);
   if (a->T == 0) return ok();

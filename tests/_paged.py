@@ -4,7 +4,7 @@ plain lists of tokens; used by the tests of the paged K/V cache.
 Tolerances, derived from the arithmetic of the kernels (u = 2^-23, one unit in
 the last place of an f32 sum, which the tensor cores may truncate):
   * a logit is a sum of 128 products: its error is at most
-    e = 144 u * scale * sum_d |q_d k_jd|, the largest over the visible tokens
+    e = 144 u |scale| sum_d |q_d k_jd|, the largest over the visible tokens
     (16 more for the scaling and the splits of its operands);
   * a weight exp(l - max) has a relative error of at most 2 e + 16 u (its own
     logit, the maximum's, the exponential and its argument's rounding);
@@ -83,7 +83,7 @@ def attend(q, K, V, scale):
     l = q @ K.T * scale
     lse = torch.logsumexp(l, -1)
     w = torch.exp(l - lse.unsqueeze(-1))
-    e = 144 * U * scale * (q.abs() @ K.abs().T).amax(-1)
+    e = 144 * U * abs(scale) * (q.abs() @ K.abs().T).amax(-1)
     return w @ V, lse, w, e, w @ V.abs()
 
 
@@ -131,7 +131,7 @@ def check_prompt(out, lse, q, cu, k, v, table, lens, window, sinks, scale, G):
             if window:
                 ok = ok & ((j < sinks) | (j > p - window))
             l = (qg @ K[:, g].T * scale).masked_fill(~ok, float("-inf"))
-            e = 144 * U * scale * (qg.abs() @ K[:, g].abs().T).masked_fill(~ok, 0.0).amax(-1) \
+            e = 144 * U * abs(scale) * (qg.abs() @ K[:, g].abs().T).masked_fill(~ok, 0.0).amax(-1) \
                 if lens[r] else torch.zeros(b - a, H, dtype=torch.float64, device=q.device)
             ls = torch.logsumexp(l, -1)
             w = torch.where(ok, torch.exp(l - ls.unsqueeze(-1)), 0.0)

@@ -392,6 +392,50 @@ def test_prompt_bad_page(kvs):
     assert float((out[99] - o).abs().max()) < 0.03 and float((lse[99] - ls).abs().max()) < 1e-4
 
 
+@pytest.mark.parametrize("scale", [-0.25, 1.0, 1e-3])
+def test_scales(kvs, scale):
+    lens = [200, 333]
+    k, v, table, n = ref.make(lens, 2, 32, seed=23)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(300, 4, D, device=DEV).to(torch.bfloat16)
+    cu = [0, 200, 300]
+    out, lse = kvs.paged_prompt_attn(q, torch.tensor(cu, dtype=torch.int32, device=DEV), cache, scale=scale)
+    ref.check_prompt(out, lse, q, cu, k, v, table, lens, 0, 0, scale, 2)
+    q = torch.randn(2, 2, 4, D, device=DEV)
+    out, lse = kvs.paged_decode_attn(q, cache, scale=scale)
+    ref.check_decode(out, lse, q, k, v, table, lens, 0, 0, scale)
+
+
+def test_prompt_offsets_out_of_range(kvs):
+    """Offsets beyond the packed rows are cut off there."""
+    k, v, table, n = ref.make([50, 50], 1, 16, seed=24)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(40, 2, D, device=DEV).to(torch.bfloat16)
+    st = _status()
+    out, lse = kvs.paged_prompt_attn(q, torch.tensor([-5, 30, 1 << 30], dtype=torch.int32, device=DEV), cache,
+                                     dev_status=st)
+    assert int(st) == kvs.KVS_EBOUNDS
+    ref.check_prompt(out, lse, q, [0, 30, 40], k, v, table, [50, 50], 0, 0, SC, 1)
+
+
+def test_prompt_growing_logits(kvs):
+    """Each token's logit is larger than all before it, and the reverse: the output is rescaled again and
+    again, and not at all. Values that no query sees are NaN."""
+    lens = [600, 600]
+    k, v, table, n = ref.make(lens, 1, 64, seed=25)
+    for r in range(2):
+        for j in range(600):
+            pg = int(table[r, j // 64])
+            k[pg, 0, j % 64] = 0.0
+            k[pg, 0, j % 64, 0] = float(j if r == 0 else 600 - j)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.zeros(700, 4, D, dtype=torch.bfloat16, device=DEV)
+    q[:, 0, 0], q[:, 1, 0], q[:, 2, 0], q[:, 3, 0] = 0.01, 1.0, 20.0, 300.0
+    cu = [0, 400, 700]
+    out, lse = kvs.paged_prompt_attn(q, torch.tensor(cu, dtype=torch.int32, device=DEV), cache)
+    ref.check_prompt(out, lse, q, cu, k, v, table, lens, 0, 0, SC, 1)
+
+
 def test_prompt_stream_and_graph(kvs):
     k, v, table, n = ref.make([400, 60], 2, 16, seed=15, poison=False)
     cache = kvs.PagedKV(k, v, table, n)

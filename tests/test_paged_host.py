@@ -68,7 +68,7 @@ def test_append_checks(kvs, args, word):
 
 @pytest.mark.parametrize("change,status", [
     (dict(q=None), 1), (dict(out=None), 1), (dict(q_dtype=2), 1), (dict(H=0), 1), (dict(H=9), 1),
-    (dict(window=-1), 1), (dict(sinks=-1), 1), (dict(mass=4096), 1), (dict(mass_out=4096), 1), (dict(q=4100), 1),
+    (dict(window=-1), 1), (dict(sinks=-1), 1), (dict(scale=0.0), 1), (dict(scale=float("nan")), 1), (dict(mass=4096), 1), (dict(mass_out=4096), 1), (dict(q=4100), 1),
     (dict(out=4100), 1)])
 def test_decode_checks(kvs, change, status):
     kv = _kv(kvs)
@@ -81,7 +81,7 @@ def test_decode_checks(kvs, change, status):
 
 @pytest.mark.parametrize("change,status", [
     (dict(q=None), 1), (dict(out=None), 1), (dict(cu=None), 1), (dict(T=-1), 1), (dict(H=0), 1), (dict(H=9), 1),
-    (dict(window=-1), 1), (dict(sinks=-5), 1), (dict(q_ld=1020), 1), (dict(q_ld=512), 1), (dict(out_ld=1028), 1),
+    (dict(window=-1), 1), (dict(sinks=-5), 1), (dict(scale=float("inf")), 1), (dict(q_ld=1020), 1), (dict(q_ld=512), 1), (dict(out_ld=1028), 1),
     (dict(q=4104), 1), (dict(out=4104), 1), (dict(T=1 << 30), 2)])
 def test_prompt_checks(kvs, change, status):
     kv = _kv(kvs)
