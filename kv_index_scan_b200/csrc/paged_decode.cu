@@ -77,7 +77,7 @@ struct DecodeParams {
   float* part;     // [blocks][kPartSlots][H][kPartRow]
   float* lse2;     // [R*G][H], base 2, of rows that one block finished (weights only)
   float* logits;   // [R*G][cap][hp], base 2 (weights only)
-  int hp;          // H rounded up to an even number
+  int hp;          // H rounded up to 2, 4 or 8
   int blocks;
   int32_t* dev_status;
 };
@@ -510,15 +510,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
   }
 }
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
+constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinTokens = 2048;  // tokens of a row that one block turns into weights
 
 // Row u's parts joined (block x = 0 of the row), and its weights (every block).
+// The lengths are read before the wait on the attention kernel: every block of
+// that kernel had waited for whatever came before it when this one was let go.
 template <bool kWeights>
 __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const DecodeParams p, int chunks) {
-  __shared__ int64_t scan_part[kJoinThreads / 32];
+  __shared__ int64_t scan_part[2][kJoinWarps];
   __shared__ float s_lse2[8];
-  pdl_wait();
+  __shared__ float s_sum[kJoinWarps][kD];
   const float ninf = -__int_as_float(0x7f800000);
   const PagedView& kv = p.kv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -533,9 +536,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const D
     if (x < r) before += c;
   }
   int64_t U, base;
-  block_scan<kJoinThreads>(all, scan_part, U);
-  __syncthreads();
-  block_scan<kJoinThreads>(before, scan_part, base);
+  block_scan<kJoinThreads>(all, scan_part[0], U);
+  block_scan<kJoinThreads>(before, scan_part[1], base);
   U *= kv.G;
   base = base * kv.G + static_cast<int64_t>(g) * vt.count;
   int b0 = 0, b1 = 0;
@@ -544,6 +546,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const D
     b0 = block_of_unit(U, base, nb);
     b1 = block_of_unit(U, base + vt.count - 1, nb);
   }
+  pdl_wait();
   if (vt.count == 0) {
     for (int e = tid; e < H * kD; e += kJoinThreads) p.out[static_cast<size_t>(u) * H * kD + e] = 0.f;
     if (p.lse && tid < H) p.lse[static_cast<size_t>(u) * H + tid] = ninf;
@@ -553,58 +556,89 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const D
     if (!kWeights) return;
     if (tid < H) s_lse2[tid] = p.lse2[static_cast<size_t>(u) * H + tid];
   } else {
-    // part x: block b0 + x, in its second slot where the row begins
+    // part x: block b0 + x, in its second slot where the row begins. A head's
+    // parts are dealt to `ways` warps, each of which finds their maximum and
+    // sum for itself and adds up its own outputs.
     const int parts = b1 - b0 + 1;
-    auto part = [&](int x, int h) {
-      return p.part + ((static_cast<size_t>(b0 + x) * kPartSlots + (x == 0 ? 1 : 0)) * H + h) * kPartRow;
-    };
-    if (warp < H) {
-      const int h = warp;
-      float M = ninf;
-      for (int x = lane; x < parts; x += 32) M = fmaxf(M, part(x, h)[0]);
+    const int shift = H <= 1 ? 0 : (H <= 2 ? 1 : (H <= 4 ? 2 : 3)), heads = 1 << shift, ways = kJoinWarps >> shift;
+    const int h = warp & (heads - 1), way = warp >> shift;
+    if (h < H) {
+      const int64_t slot = static_cast<int64_t>(H) * kPartRow;
+      const float* const first = p.part + (static_cast<int64_t>(b0) * kPartSlots + 1) * slot + h * kPartRow;
+      const float* const rest = first - slot;
+      auto part = [&](int x) { return x == 0 ? first : rest + x * kPartSlots * slot; };
+      float M = ninf, L = 0.f;  // of the parts lane, lane + 32, ...
+      for (int x = lane; x < parts; x += 32) {
+        const float2 v = *reinterpret_cast<const float2*>(part(x));
+        const float m = fmaxf(M, v.x), f = m == ninf ? 0.f : m;
+        L = L * exp2f(M - f) + v.y * exp2f(v.x - f);
+        M = m;
+      }
+      float f = M;
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
-      const float f = M == ninf ? 0.f : M;
-      float L = 0.f;
-      for (int x = lane; x < parts; x += 32) L = fmaf(part(x, h)[1], exp2f(part(x, h)[0] - f), L);
+      for (int d = 16; d > 0; d >>= 1) f = fmaxf(f, __shfl_xor_sync(0xFFFFFFFFu, f, d));
+      const float top = f;
+      if (f == ninf) f = 0.f;
+      L *= exp2f(M - f);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, d);
-      const float z = L == 0.f ? ninf : M + log2f(L);
-      if (lane == 0) s_lse2[h] = z;
+      const float z = L == 0.f ? ninf : top + log2f(L);
+      if (way == 0 && lane == 0) {
+        s_lse2[h] = z;
+        if (p.lse && chunk == 0) p.lse[static_cast<size_t>(u) * H + h] = z * 0.6931471805599453f;
+      }
       if (chunk == 0) {
+        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int x = 0; x < parts; ++x) {
-          const float* pp = part(x, h);
-          const float c = exp2f(pp[0] - f);
+        for (int x = way; x < parts; x += ways) {
+          const float* pp = part(x);
+          const float c = exp2f(pp[0] - f) * inv;
           const float4 v = *reinterpret_cast<const float4*>(pp + 4 + 4 * lane);
           acc.x = fmaf(c, v.x, acc.x);
           acc.y = fmaf(c, v.y, acc.y);
           acc.z = fmaf(c, v.z, acc.z);
           acc.w = fmaf(c, v.w, acc.w);
         }
-        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-        *reinterpret_cast<float4*>(p.out + (static_cast<size_t>(u) * H + h) * kD + 4 * lane) =
-            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (p.lse && lane == 0) p.lse[static_cast<size_t>(u) * H + h] = z * 0.6931471805599453f;
+        *reinterpret_cast<float4*>(&s_sum[warp][4 * lane]) = acc;
       }
     }
+    __syncthreads();
+    if (chunk == 0)
+      for (int e = tid; e < H * kD; e += kJoinThreads) {
+        float o = 0.f;
+        for (int w = 0; w < min(ways, parts); ++w) o += s_sum[w * heads + e / kD][e % kD];
+        p.out[static_cast<size_t>(u) * H * kD + e] = o;
+      }
   }
   if constexpr (kWeights) {
     __syncthreads();
     const size_t row = static_cast<size_t>(u) * kv.cap();
+    float z[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h) z[h] = h < H ? s_lse2[h] : ninf;
+#pragma unroll
     for (int e = tid; e < kJoinTokens; e += kJoinThreads) {
       const int k = chunk * (kJoinTokens / kUnit) + e / kUnit;
       if (k >= vt.count) break;
       const int t = vt.tile(k) * kUnit + e % kUnit;
       if (t >= vt.end || (t < vt.lo && t >= p.sinks)) continue;
       const float* l = p.logits + (row + t) * p.hp;
+      const float m = p.mass[row + t];
       float w = 0.f;
-      for (int h = 0; h < H; ++h) {
-        const float z = s_lse2[h];
-        w += z == ninf ? 0.f : exp2f(l[h] - z);
+      auto add = [&](float x, int h) { w += z[h] == ninf ? 0.f : exp2f(x - z[h]); };
+      if (p.hp == 2) {
+        const float2 v = *reinterpret_cast<const float2*>(l);
+        add(v.x, 0), add(v.y, 1);
+      } else {
+        const float4 v = *reinterpret_cast<const float4*>(l);
+        add(v.x, 0), add(v.y, 1), add(v.z, 2), add(v.w, 3);
+        if (p.hp == 8) {
+          const float4 y = *reinterpret_cast<const float4*>(l + 4);
+          add(y.x, 4), add(y.y, 5), add(y.z, 6), add(y.w, 7);
+        }
       }
-      p.mass_out[row + t] = p.mass[row + t] + w;
+      p.mass_out[row + t] = m + w;
     }
   }
 }
@@ -613,7 +647,7 @@ int decode_blocks() { return kBlocksPerSM * sm_count(); }
 
 size_t carve(DecodeParams* p, void* ws, int R, int G, int H, int weight_cap) {
   WsCarver c(ws);
-  const int hp = (H + 1) / 2 * 2;
+  const int hp = H <= 2 ? 2 : (H <= 4 ? 4 : 8);
   float* part = c.take<float>(static_cast<size_t>(decode_blocks()) * kPartSlots * H * kPartRow);
   float* lse2 = weight_cap ? c.take<float>(static_cast<size_t>(R) * G * H) : nullptr;
   float* logits = weight_cap ? c.take<float>(static_cast<size_t>(R) * G * weight_cap * hp) : nullptr;

@@ -9,18 +9,37 @@
 // one. Sources lie behind the budget and destinations before it, so the moves
 // need no order among themselves.
 //
-// Two kernels. The selection (one block per (r, g)) finds the budget-th largest
-// key by a radix select and lists which slot each kept one comes from; the move
-// (the whole grid) copies 512 bytes for each slot whose token came from another.
+// A cluster of blocks takes each (r, g) row, so that a few long rows occupy the
+// GPU as well as many short ones:
+//  1. each block turns its run of the row's slots into 32-bit keys in shared
+//     memory and writes the slots' own values
+//     out;
+//  2. the budget-th largest key by a radix select in digits of 11, 11 and 10
+//     bits: histograms in shared memory, summed over the cluster by distributed
+//     shared memory, every block finding the digit for itself;
+//  3. each thread counts holes and movers in a contiguous piece of its block's
+//     run; ranks by a scan over the block and the cluster; the two lists go to
+//     the workspace;
+//  4. the cluster's warps share the moves: 512 bytes each, several rows in
+//     flight per warp.
+// Ties at the cut go to the lower slots: only then the tied keys are ranked too.
+// Bound by the moved rows' bytes, for small moves by the latency of the steps.
+#include <cooperative_groups.h>
+
 #include "paged.cuh"
 
 namespace kvs {
 
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kMoveWarps = 8;
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+constexpr int kKeysMost = 22 * 1024;  // keys of a block in shared memory (two blocks share an SM)
+constexpr int kFlight = 8;            // rows that a warp copies at a time
 
 struct EvictParams {
   PagedView kv;
@@ -30,39 +49,56 @@ struct EvictParams {
   int budget, sinks, recent;
   float* mass_out;
   int32_t* pos_out;
-  int32_t* n_out;
+  int32_t* n_out;  // written here where it is not n itself
   int32_t* src;
-  int32_t* holes;  // [R*G][budget]
+  int32_t* holes;   // [R*G][budget]
+  int32_t* movers;  // [R*G][budget]
+  int keys_room;    // keys of shared memory a block has
   int32_t* dev_status;
 };
 
-// Exclusive rank of `p` among the block's threads in thread order, and the
-// total. `part` is kSelWarps ints of shared memory, free again on return.
-__device__ __forceinline__ int block_rank(bool p, int* part, int& total) {
+struct EvictShared {
+  int hist[3][kBins];  // one a digit: no block clears what another still reads
+  unsigned long long part[kWarps];
+  unsigned long long count;  // of this block, read by its cluster
+  int digit, need, equal;
+};
+
+// Sum over the block of v, and the sum of the threads before this one.
+__device__ __forceinline__ unsigned long long scan_block(unsigned long long v, unsigned long long* part,
+                                                         unsigned long long& total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned m = __ballot_sync(0xFFFFFFFFu, p);
-  if (lane == 0) part[warp] = __popc(m);
-  __syncthreads();
-  int x = part[lane];  // kSelWarps == 32
-  int inc = x;
+  unsigned long long inc = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+    const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, inc, d);
     if (lane >= d) inc += y;
   }
-  total = __shfl_sync(0xFFFFFFFFu, inc, 31);
-  const int before = __shfl_sync(0xFFFFFFFFu, inc - x, warp);
+  if (lane == 31) part[warp] = inc;
   __syncthreads();
-  return before + __popc(m & ((1u << lane) - 1u));
+  const unsigned long long x = lane < kWarps ? part[lane] : 0ull;
+  unsigned long long w = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, w, d);
+    if (lane >= d) w += y;
+  }
+  total = __shfl_sync(0xFFFFFFFFu, w, 31);
+  const unsigned long long before = __shfl_sync(0xFFFFFFFFu, w - x, warp);
+  __syncthreads();
+  return before + inc - v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p) {
+__global__ void __launch_bounds__(kThreads, 2) paged_evict_kernel(EvictParams p) {
+  extern __shared__ uint32_t evict_keys[];
+  __shared__ EvictShared sm;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int e = tid; e < 3 * kBins; e += kThreads) sm.hist[0][e] = 0;
   pdl_wait();
-  __shared__ int hist[256];
-  __shared__ int part[kSelWarps];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
-  const int u = blockIdx.x, r = u / p.kv.G;
+  pdl_trigger();
+  const int u = blockIdx.x / C, r = u / p.kv.G, g = u % p.kv.G;
   const int n = p.kv.length(r, p.dev_status);
   const int seen = p.seen ? p.seen[r] : n;
   const int b = p.budget;
@@ -72,107 +108,188 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
   float* mass_out = p.mass_out + row;
   int32_t* pos_out = p.pos_out ? p.pos_out + row : nullptr;
   int32_t* src = p.src + static_cast<size_t>(u) * b;
-  int32_t* holes = p.holes + static_cast<size_t>(u) * b;
-  auto put = [&](int j, int from) {
-    src[j] = from;
-    mass_out[j] = mass[from];
-    if (pos_out) pos_out[j] = pos[from];
-  };
-  if (n <= b) {
-    for (int j = threadIdx.x; j < b; j += kSelThreads) {
-      if (j < n) put(j, j);
-      else src[j] = -1;
-    }
-    return;
-  }
-  // the order of slots: protected ones above any weight, NaN below any
-  auto key = [&](int j) -> uint32_t {
-    const int at = pos ? pos[j] : j;
+  if (p.n_out && g == 0 && rank == 0 && tid == 0) p.n_out[r] = min(n, b);
+
+  // every slot's own values; where the budget is not reached they are all
+  const bool over = n > b;
+  const int per = over ? (n + C - 1) / C : (b + C - 1) / C;
+  const int lo = min(rank * per, over ? n : b), hi = min(lo + per, over ? n : b);
+  const bool in_smem = per <= p.keys_room;
+  auto key_of = [&](float m, int at) -> uint32_t {
+    // protected ones above any weight, NaN below any
     if (at < p.sinks || at >= seen - p.recent) return 0xFFFFFFFFu;
-    const float m = mass[j];
     return m != m ? 0u : ordered_key(m);
   };
-  // the b-th largest key, eight bits at a time
-  uint32_t prefix = 0;
-  int need = b;  // still to take among the keys that share the prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (threadIdx.x < 256) hist[threadIdx.x] = 0;
-    __syncthreads();
-    for (int j = threadIdx.x; j < n; j += kSelThreads) {
-      const uint32_t k = key(j);
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1);
+#pragma unroll 4
+  for (int j = lo + tid; j < hi; j += kThreads) {
+    float m = 0.f;
+    int at = j;
+    if (j < n) {
+      m = mass[j];
+      if (pos) at = pos[j];
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      int d = 255, left = need;
-      while (hist[d] < left) left -= hist[d--];
-      s_prefix = prefix | (static_cast<uint32_t>(d) << shift);
-      s_need = left;
+    if (j < b) {
+      src[j] = j < n ? j : -1;
+      if (j < n && mass_out != mass) mass_out[j] = m;
+      if (j < n && pos_out != pos) pos_out[j] = at;
     }
-    __syncthreads();
-    prefix = s_prefix;
-    need = s_need;
+    if (over && in_smem) evict_keys[j - lo] = key_of(m, at);
   }
-  // kept: keys above the cut, and of those at it the `need` lowest slots
-  int ties = 0, nh = 0, nm = 0;
-  for (int j0 = 0; j0 < n; j0 += kSelThreads) {
-    const int j = j0 + threadIdx.x;
-    const uint32_t k = j < n ? key(j) : 0u;
-    const bool tie = j < n && k == prefix;
-    int total;
-    const int tr = ties + block_rank(tie, part, total);
-    ties += total;
-    const bool keep = j < n && (k > prefix || (tie && tr < need));
-    const bool hole = j < b && !keep, mover = j >= b && keep;
-    const int hr = nh + block_rank(hole, part, total);
-    nh += total;
-    const int mr = nm + block_rank(mover, part, total);
-    nm += total;
-    if (hole) holes[hr] = j;
-    if (j < b && keep) put(j, j);
-    __syncthreads();  // holes are written before a mover reads them
-    if (mover) put(holes[mr], j);
+  if (!over) return;  // (the whole cluster)
+  auto key = [&](int j) { return in_smem ? evict_keys[j - lo] : key_of(mass[j], pos ? pos[j] : j); };
+  __syncthreads();
+
+  // the b-th largest key
+  uint32_t cut = 0;
+  int need = b, equal = 0;  // still to take among the keys that share the cut's digits, and how many do
+  constexpr int kShift[3] = {21, 10, 0};
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = kShift[pass], width = pass == 2 ? 10 : 11;
+    int* hist = sm.hist[pass];
+    for (int j0 = lo; j0 < hi; j0 += kThreads) {
+      const int j = j0 + tid;
+      const uint32_t k = j < hi ? key(j) : 0u;
+      const bool mine = j < hi && (pass == 0 || (k >> (shift + width)) == (cut >> (shift + width)));
+      // heavy bins are common (equal weights, the protected): one add for the
+      // lanes that share lane 0's bin, the others by themselves
+      const uint32_t d = (k >> shift) & ((1u << width) - 1u);
+      const unsigned act = __ballot_sync(0xFFFFFFFFu, mine);
+      if (act) {
+        const int lead = __ffs(act) - 1;
+        const uint32_t d0 = __shfl_sync(0xFFFFFFFFu, d, lead);
+        const unsigned same = __ballot_sync(0xFFFFFFFFu, mine && d == d0);
+        if (lane == lead) atomicAdd(&hist[d0], __popc(same));
+        else if (mine && d != d0) atomicAdd(&hist[d], 1);
+      }
+    }
+    cluster.sync();
+    // bins from the top, kOwn a thread
+    constexpr int kOwn = kBins / kThreads;
+    static_assert(kOwn == 4, "a thread's bins are one 16-byte load");
+    const int bin = kBins - kOwn * (tid + 1);
+    int h[kOwn] = {0, 0, 0, 0};
+    for (int x = 0; x < C; ++x) {
+      const int4 v = *reinterpret_cast<const int4*>(cluster.map_shared_rank(hist, x) + bin);
+      h[0] += v.x;
+      h[1] += v.y;
+      h[2] += v.z;
+      h[3] += v.w;
+    }
+    unsigned long long all;
+    int above = static_cast<int>(scan_block(static_cast<unsigned long long>(h[0] + h[1] + h[2] + h[3]), sm.part, all));
+#pragma unroll
+    for (int e = kOwn - 1; e >= 0; --e) {
+      if (above < need && above + h[e] >= need) {
+        sm.digit = bin + e;
+        sm.need = need - above;
+        sm.equal = h[e];
+      }
+      above += h[e];
+    }
+    __syncthreads();
+    cut |= static_cast<uint32_t>(sm.digit) << shift;
+    need = sm.need;
+    equal = sm.equal;
+    __syncthreads();
+  }
+
+  // this thread's piece of the block's run (an odd length: no bank conflicts)
+  const int len = ((hi - lo + kThreads - 1) / kThreads) | 1;
+  const int a0 = min(lo + tid * len, hi), a1 = min(a0 + len, hi);
+  unsigned long long total;
+  auto before_us = [&](unsigned long long mine) {  // sums of the cluster's blocks before this one
+    if (tid == 0) sm.count = mine;
+    cluster.sync();
+    unsigned long long s = 0;
+    for (int x = 0; x < rank; ++x) s += *cluster.map_shared_rank(&sm.count, x);
+    return s;
+  };
+  int tie = 0;  // rank of the next tied key of this thread
+  const bool some = equal > need;  // only some of the tied keys are kept
+  if (some) {
+    int t = 0;
+    for (int j = a0; j < a1; ++j) t += key(j) == cut;
+    const unsigned long long mine = scan_block(t, sm.part, total);
+    tie = static_cast<int>(before_us(total) + mine);
+    cluster.sync();  // every block has read the counts
+  }
+  const int tie0 = tie;
+  auto kept = [&](uint32_t k) { return k > cut || (k == cut && (!some || tie++ < need)); };
+  unsigned long long moves = 0;  // holes, and movers in the upper half
+  for (int j = a0; j < a1; ++j) {
+    const bool keep = kept(key(j));
+    if (j < b) moves += keep ? 0ull : 1ull;
+    else moves += keep ? 1ull << 32 : 0ull;
+  }
+  unsigned long long at = scan_block(moves, sm.part, total);
+  at += before_us(total);
+  {
+    int h = static_cast<int>(at & 0xFFFFFFFFull), m = static_cast<int>(at >> 32);
+    int32_t* holes = p.holes + static_cast<size_t>(u) * b;
+    int32_t* movers = p.movers + static_cast<size_t>(u) * b;
+    tie = tie0;
+    for (int j = a0; j < a1; ++j) {
+      const bool keep = kept(key(j));
+      if (j < b && !keep) holes[h++] = j;
+      if (j >= b && keep) movers[m++] = j;
+    }
+  }
+  unsigned long long last = 0;  // moves in all
+  for (int x = 0; x < C; ++x) last += *cluster.map_shared_rank(&sm.count, x);
+  cluster.sync();  // the lists are written, and every block has read the counts
+  const int count = static_cast<int>(last & 0xFFFFFFFFull);
+
+  // the moves, 32 a warp at a time
+  const int32_t* holes = p.holes + static_cast<size_t>(u) * b;
+  const int32_t* movers = p.movers + static_cast<size_t>(u) * b;
+  const bool isv = lane >= 16;
+  uint16_t* pool = (isv ? p.kv.V : p.kv.K) + 8 * (lane & 15);
+  // moves k0 + x * C * kWarps ...: spread so that few moves reach every warp
+  const int workers = C * kWarps, me = rank * kWarps + warp;
+  const int chunk = min(32, (count + workers - 1) / workers);
+  for (int k0 = me * chunk; k0 < count; k0 += workers * chunk) {
+    const int k = k0 + lane;
+    int64_t from = -1, to = -1;
+    if (lane < chunk && k < count) {
+      const int h = __ldcg(holes + k), s = __ldcg(movers + k);
+      src[h] = s;
+      mass_out[h] = mass[s];
+      if (pos_out) pos_out[h] = pos[s];
+      const int ps = p.kv.page_of(r, s, p.dev_status), ph = p.kv.page_of(r, h, p.dev_status);
+      if (ps >= 0 && ph >= 0) {
+        from = p.kv.row(ps, g, s);
+        to = p.kv.row(ph, g, h);
+      }
+    }
+    const int here = min(chunk, count - k0);
+    for (int x0 = 0; x0 < here; x0 += kFlight) {
+      uint4 v[kFlight];
+#pragma unroll
+      for (int x = 0; x < kFlight; ++x) {
+        const int64_t f = __shfl_sync(0xFFFFFFFFu, from, (x0 + x) & 31);
+        if (x0 + x < here && f >= 0) v[x] = *reinterpret_cast<const uint4*>(pool + f);
+      }
+#pragma unroll
+      for (int x = 0; x < kFlight; ++x) {
+        const int64_t t = __shfl_sync(0xFFFFFFFFu, to, (x0 + x) & 31);
+        if (x0 + x < here && t >= 0) *reinterpret_cast<uint4*>(pool + t) = v[x];
+      }
+    }
   }
 }
 
-__global__ void __launch_bounds__(32 * kMoveWarps) evict_move_kernel(EvictParams p) {
+// n cut to the budget in place, once no block needs it any more.
+__global__ void evict_length_kernel(PagedView kv, int budget, int32_t* n) {
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t warp0 = static_cast<int64_t>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * kMoveWarps;
-  const int per = (p.budget + 31) / 32;
-  const int64_t items = static_cast<int64_t>(p.kv.R) * p.kv.G * per;
-  for (int64_t it = warp0; it < items; it += warps) {
-    const int u = static_cast<int>(it / per), r = u / p.kv.G, g = u % p.kv.G;
-    const int j = static_cast<int>(it % per) * 32 + lane;
-    const int from = j < p.budget ? p.src[static_cast<size_t>(u) * p.budget + j] : -1;
-    unsigned todo = __ballot_sync(0xFFFFFFFFu, from >= 0 && from != j);
-    int64_t a = -1, b = -1;
-    if (from >= 0 && from != j) {
-      const int pa = p.kv.page_of(r, from, p.dev_status), pb = p.kv.page_of(r, j, p.dev_status);
-      if (pa >= 0 && pb >= 0) {
-        a = p.kv.row(pa, g, from);
-        b = p.kv.row(pb, g, j);
-      }
-    }
-    const bool isv = lane >= 16;
-    uint16_t* pool = (isv ? p.kv.V : p.kv.K) + 8 * (lane & 15);
-    while (todo) {
-      const int l = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const int64_t fa = __shfl_sync(0xFFFFFFFFu, a, l), fb = __shfl_sync(0xFFFFFFFFu, b, l);
-      if (fa >= 0) *reinterpret_cast<uint4*>(pool + fb) = *reinterpret_cast<const uint4*>(pool + fa);
-    }
-  }
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; r < p.kv.R;
-       r += static_cast<int64_t>(gridDim.x) * blockDim.x)
-    p.n_out[r] = min(p.kv.length(static_cast<int>(r), nullptr), p.budget);
+  const int r = blockIdx.x * blockDim.x + threadIdx.x;
+  if (r < kv.R) n[r] = min(kv.length(r, nullptr), budget);
 }
 
 }  // namespace
 
 size_t paged_evict_ws_bytes(int R, int G, int budget) {
-  return align_up(static_cast<size_t>(R) * G * budget * sizeof(int32_t), 16);
+  return align_up(2 * static_cast<size_t>(R) * G * budget * sizeof(int32_t), 16);
 }
 
 kvs_status paged_evict_launch(const kvs_paged_evict_args* a, void* ws, int32_t* dev_status, cudaStream_t s) {
@@ -186,16 +303,40 @@ kvs_status paged_evict_launch(const kvs_paged_evict_args* a, void* ws, int32_t* 
   p.recent = a->recent;
   p.mass_out = a->mass_out;
   p.pos_out = a->pos_out;
-  p.n_out = a->n_out;
+  const bool in_place = a->n_out == a->kv->n;
+  p.n_out = in_place ? nullptr : a->n_out;
   p.src = a->src;
-  p.holes = static_cast<int32_t*>(ws);
-  p.dev_status = dev_status;
   const int RG = p.kv.R * p.kv.G;
-  launch_chained(evict_select_kernel, dim3(RG), dim3(kSelThreads), 0, s, p);
-  const int64_t items = static_cast<int64_t>(RG) * ((a->budget + 31) / 32);
-  const int64_t want = (items + kMoveWarps - 1) / kMoveWarps;
-  const int grid = static_cast<int>(want < 8ll * sm_count() ? want : 8ll * sm_count());
-  launch_chained(evict_move_kernel, dim3(grid), dim3(32 * kMoveWarps), 0, s, p);
+  p.holes = static_cast<int32_t*>(ws);
+  p.movers = p.holes + static_cast<size_t>(RG) * a->budget;
+  p.dev_status = dev_status;
+  // blocks a row: enough to occupy two on every SM, each with at least a
+  // thousand slots of the longest row there may be
+  const int64_t cap = static_cast<int64_t>(a->kv->max_pages) * a->kv->page;
+  int C = 1;
+  while (C < kMaxCluster && static_cast<int64_t>(RG) * C * 2 <= 2 * sm_count() && cap / (2 * C) >= 1024) C *= 2;
+  const int64_t most = (cap + C - 1) / C;
+  p.keys_room = static_cast<int>(most < kKeysMost ? most : kKeysMost);
+  const size_t smem = static_cast<size_t>(p.keys_room) * sizeof(uint32_t);
+  cudaFuncSetAttribute(paged_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       kKeysMost * static_cast<int>(sizeof(uint32_t)));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(RG) * C);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaLaunchKernelEx(&cfg, paged_evict_kernel, p);
+  if (in_place)
+    launch_chained(evict_length_kernel, dim3((p.kv.R + 127) / 128), dim3(128), 0, s, p.kv, a->budget, a->n_out);
   return check_launch("kvs_paged_evict");
 }
 

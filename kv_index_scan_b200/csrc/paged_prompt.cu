@@ -44,7 +44,9 @@ constexpr int kTileBytes = 2 * kHalfBytes;   // 128 rows of 128 bf16
 constexpr int kStages = 2;                   // of K, and of V
 constexpr int kInfos = 4;
 constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
-constexpr int kThreads = 32 * 11;
+constexpr int kThreads = 32 * 12;             // three warpgroups; the last warp is idle
+// registers a thread: 168 at launch; 8 * 208 + 4 * 88 = 12 * 168
+constexpr int kSoftRegs = 208, kOtherRegs = 88;
 constexpr float kGrow = 8.f;                 // log2 of the growth that a maximum may lag behind
 
 struct PromptSmem {
@@ -52,7 +54,7 @@ struct PromptSmem {
   unsigned char k[kStages][kTileBytes];
   unsigned char v[kStages][kTileBytes];
   uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_clean[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full by tile and half of the tokens
   int groups[kInfos];  // by tile: which 16-token groups were loaded
   uint32_t tmem;
   int abort_flag;
@@ -158,6 +160,25 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
+// two f32 in a register pair
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 // bits [0, x) of a word
 __device__ __forceinline__ uint32_t low_bits(int x) { return x <= 0 ? 0u : (x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1u); }
 
@@ -242,7 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], kRows);
+      mbar_init(&sm.p_full[i][0], kRows);
+      mbar_init(&sm.p_full[i][1], kRows);
       mbar_init(&sm.o_full[i], 1);
     }
     sm.abort_flag = 0;
@@ -269,128 +291,135 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
     return false;
   };
 
-  if (warp == kLoadWarp) {
-    // ---------------- K and V tiles ----------------
-    const int box = min(1 << kv.shift, kTok), pages = kTok / box;
-    const int half = lane & 1, sub = lane >> 1;
-    int issued = 0;
-    // this lane's page of tile i
-    auto look = [&](int i) {
-      const int t = tile_token(i) + sub * box;
-      if (sub >= pages || t >= end || (t >= p.sinks && t + box <= lo)) return -1;
-      return kv.page_of(r, t, p.dev_status);
-    };
-    int next = tiles > 0 ? look(0) : -1;
-    for (int i = 0; i < tiles; ++i) {
-      const int st = i % kStages;
-      const int id = next;
-      if (i + 1 < tiles) next = look(i + 1);
-      const unsigned have = __ballot_sync(0xFFFFFFFFu, id >= 0);
-      const int in_page = (tile_token(i) + sub * box) & ((1 << kv.shift) - 1);
-      const uint32_t at = half * kHalfBytes + sub * box * 128;
-      for (int which = 0; which < 2; ++which) {
-        uint64_t* full = which ? &sm.v_full[st] : &sm.k_full[st];
-        int ok = 1;
-        if (lane == 0) {
-          if (i >= kStages) ok = wait(which ? &sm.v_empty[st] : &sm.k_empty[st], (i / kStages - 1) & 1);
-          if (ok) {
-            if (which == 0) {
-              int there = 0;
-              for (int e = 0; e < 8; ++e)
-                if (have >> (2 * (16 * e / box)) & 1u) there |= 1 << e;
-              sm.groups[i % kInfos] = there;
-              __threadfence_block();
-            }
-            if (have) mbar_expect(full, __popc(have) * box * 128);
-            else mbar_arrive(full);
-          }
-        }
-        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-        if (!ok) break;
-        if (id >= 0)
-          tma_page_rows(sm_addr(which ? sm.v[st] : sm.k[st]) + at, which ? &mapV : &mapK, in_page, half, g, id, full);
-        issued = 2 * i + which + 1;
-      }
-      if (issued < 2 * i + 2) break;
-    }
-    // no copy may be in flight when the block ends
-    if (lane == 0)
-      for (int x = max(0, issued - 2 * kStages); x < issued; ++x) {
-        const int i = x / 2;
-        mbar_wait(x & 1 ? &sm.v_full[i % kStages] : &sm.k_full[i % kStages], (i / kStages) & 1);
-      }
-  } else if (warp == kCleanWarp) {
-    // ---------------- rows of V that no row of the block sees ----------------
-    for (int i = 0; i < tiles; ++i) {
-      const int st = i % kStages;
-      int ok = 1;
-      if (lane == 0) ok = wait(&sm.v_full[st], (i / kStages) & 1);
-      if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
-      const int t0 = tile_token(i), there = sm.groups[i % kInfos];
-      if (there != 0xFF || t0 + kTok > end || (t0 < lo && t0 + kTok > p.sinks)) {
-        for (int x = lane; x < kTok * 16; x += 32) {
-          const int row = x >> 4, t = t0 + row;
-          if ((there >> (row >> 4) & 1) && t < end && (t >= lo || t < p.sinks)) continue;
-          *reinterpret_cast<uint4*>(sm.v[st] + (x >> 3 & 1) * kHalfBytes + row * 128 + (x & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        __syncwarp();
-      }
-      if (lane == 0) mbar_arrive(&sm.v_clean[st]);
-    }
-  } else if (warp == kMmaWarp) {
-    // ---------------- products ----------------
-    if (lane == 0 && tiles > 0) {
-      const uint64_t dq = desc_k_major(sm_addr(sm.q[0])), dk = desc_k_major(sm_addr(sm.k[0])),
-                     dv = desc_mn_major(sm_addr(sm.v[0]));
-      auto qk = [&](int t, int i) {
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const uint64_t step = (ks >> 2) * (kHalfBytes >> 4) + (ks & 3) * 2;
-          mma_ss(tmem + 128 * t, dq + t * (kTileBytes >> 4) + step, dk + (i % kStages) * (kTileBytes >> 4) + step, kIdesc,
-                 ks > 0);
-        }
-        mma_commit_to(&sm.s_full[t]);
+  if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    if (warp == kLoadWarp) {
+      // ---------------- K and V tiles ----------------
+      const int box = min(1 << kv.shift, kTok), pages = kTok / box;
+      const int half = lane & 1, sub = lane >> 1;
+      int issued = 0;
+      // this lane's page of tile i
+      auto look = [&](int i) {
+        const int t = tile_token(i) + sub * box;
+        if (sub >= pages || t >= end || (t >= p.sinks && t + box <= lo)) return -1;
+        return kv.page_of(r, t, p.dev_status);
       };
-      bool ok = wait(&sm.q_full, 0) && wait(&sm.k_full[0], 0);
-      if (ok) {
-        fence_after();
-        qk(0, 0);
-        qk(1, 0);
-        mma_commit_to(&sm.k_empty[0]);
-      }
-      for (int i = 0; i < tiles && ok; ++i) {
+      int next = tiles > 0 ? look(0) : -1;
+      for (int i = 0; i < tiles; ++i) {
         const int st = i % kStages;
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (t == 0) ok = wait(&sm.v_full[st], (i / kStages) & 1) && wait(&sm.v_clean[st], (i / kStages) & 1);
-          ok = ok && wait(&sm.p_full[t], i & 1);
+        const int id = next;
+        if (i + 1 < tiles) next = look(i + 1);
+        const unsigned have = __ballot_sync(0xFFFFFFFFu, id >= 0);
+        const int in_page = (tile_token(i) + sub * box) & ((1 << kv.shift) - 1);
+        const uint32_t at = half * kHalfBytes + sub * box * 128;
+        for (int which = 0; which < 2; ++which) {
+          uint64_t* full = which ? &sm.v_full[st] : &sm.k_full[st];
+          int ok = 1;
+          if (lane == 0) {
+            if (i >= kStages) ok = wait(which ? &sm.v_empty[st] : &sm.k_empty[st], (i / kStages - 1) & 1);
+            if (ok) {
+              if (which == 0) {
+                int there = 0;
+                for (int e = 0; e < 8; ++e)
+                  if (have >> (2 * (16 * e / box)) & 1u) there |= 1 << e;
+                sm.groups[i % kInfos] = there;
+                __threadfence_block();
+              }
+              if (have) mbar_expect(full, __popc(have) * box * 128);
+              else mbar_arrive(full);
+            }
+          }
+          ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
           if (!ok) break;
-          fence_after();
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * ks, dv + st * (kTileBytes >> 4) + ks * (2048 >> 4), kIdescMn,
-                   i > 0 || ks > 0);
-          if (t == 1) mma_commit_to(&sm.v_empty[st]);
-          if (i + 1 == tiles) {
-            mma_commit_to(&sm.o_full[t]);
-            continue;
-          }
-          if (t == 0) {
-            ok = wait(&sm.k_full[(i + 1) % kStages], ((i + 1) / kStages) & 1);
-            if (!ok) break;
-            fence_after();
-          }
-          qk(t, i + 1);
-          if (t == 1) mma_commit_to(&sm.k_empty[(i + 1) % kStages]);
+          if (id >= 0)
+            tma_page_rows(sm_addr(which ? sm.v[st] : sm.k[st]) + at, which ? &mapV : &mapK, in_page, half, g, id, full);
+          issued = 2 * i + which + 1;
         }
+        if (issued < 2 * i + 2) break;
       }
-      if (!ok) {  // products already issued end before the block does
-        mma_commit_to(&sm.o_full[0]);
-        mbar_wait(&sm.o_full[0], 0);
+      // no copy may be in flight when the block ends
+      if (lane == 0)
+        for (int x = max(0, issued - 2 * kStages); x < issued; ++x) {
+          const int i = x / 2;
+          mbar_wait(x & 1 ? &sm.v_full[i % kStages] : &sm.k_full[i % kStages], (i / kStages) & 1);
+        }
+    } else if (warp == kCleanWarp) {
+      // ---------------- rows of V that no row of the block sees ----------------
+      for (int i = 0; i < tiles; ++i) {
+        const int st = i % kStages;
+        int ok = 1;
+        if (lane == 0) ok = wait(&sm.v_full[st], (i / kStages) & 1);
+        if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+        const int t0 = tile_token(i), there = sm.groups[i % kInfos];
+        if (there != 0xFF || t0 + kTok > end || (t0 < lo && t0 + kTok > p.sinks)) {
+          for (int x = lane; x < kTok * 16; x += 32) {
+            const int row = x >> 4, t = t0 + row;
+            if ((there >> (row >> 4) & 1) && t < end && (t >= lo || t < p.sinks)) continue;
+            *reinterpret_cast<uint4*>(sm.v[st] + (x >> 3 & 1) * kHalfBytes + row * 128 + (x & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(&sm.v_clean[st]);
+      }
+    } else if (warp == kMmaWarp) {
+      // ---------------- products ----------------
+      if (lane == 0 && tiles > 0) {
+        const uint64_t dq = desc_k_major(sm_addr(sm.q[0])), dk = desc_k_major(sm_addr(sm.k[0])),
+                       dv = desc_mn_major(sm_addr(sm.v[0]));
+        auto qk = [&](int t, int i) {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const uint64_t step = (ks >> 2) * (kHalfBytes >> 4) + (ks & 3) * 2;
+            mma_ss(tmem + 128 * t, dq + t * (kTileBytes >> 4) + step, dk + (i % kStages) * (kTileBytes >> 4) + step, kIdesc,
+                   ks > 0);
+          }
+          mma_commit_to(&sm.s_full[t]);
+        };
+        bool ok = wait(&sm.q_full, 0) && wait(&sm.k_full[0], 0);
+        if (ok) {
+          fence_after();
+          qk(0, 0);
+          qk(1, 0);
+          mma_commit_to(&sm.k_empty[0]);
+        }
+        for (int i = 0; i < tiles && ok; ++i) {
+          const int st = i % kStages;
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (t == 0) ok = wait(&sm.v_full[st], (i / kStages) & 1) && wait(&sm.v_clean[st], (i / kStages) & 1);
+            for (int e = 0; e < 2 && ok; ++e) {
+              ok = wait(&sm.p_full[t][e], i & 1);
+              if (!ok) break;
+              fence_after();
+#pragma unroll
+              for (int ks = 4 * e; ks < 4 * e + 4; ++ks)
+                mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * ks, dv + st * (kTileBytes >> 4) + ks * (2048 >> 4),
+                       kIdescMn, i > 0 || ks > 0);
+            }
+            if (!ok) break;
+            if (t == 1) mma_commit_to(&sm.v_empty[st]);
+            if (i + 1 == tiles) {
+              mma_commit_to(&sm.o_full[t]);
+              continue;
+            }
+            if (t == 0) {
+              ok = wait(&sm.k_full[(i + 1) % kStages], ((i + 1) / kStages) & 1);
+              if (!ok) break;
+              fence_after();
+            }
+            qk(t, i + 1);
+            if (t == 1) mma_commit_to(&sm.k_empty[(i + 1) % kStages]);
+          }
+        }
+        if (!ok) {  // products already issued end before the block does
+          mma_commit_to(&sm.o_full[0]);
+          mbar_wait(&sm.o_full[0], 0);
+        }
       }
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
     // ---------------- softmax, a row per thread ----------------
     const int t = warp >> 2;                       // row tile
     const int mine = 128 * t + (tid & 127);        // row of the block
@@ -478,24 +507,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
         }
       }
       const float f = m == ninf ? 0.f : m;
-      float z0 = 0.f, z1 = 0.f;
+      const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), f2 = pair(-f, -f);
+      uint64_t z[2] = {0, 0};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         uint32_t w[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float a = exp2_fast(fmaf(s[32 * e + 2 * j], p.scale_log2, -f));
-          const float b = exp2_fast(fmaf(s[32 * e + 2 * j + 1], p.scale_log2, -f));
-          z0 += a;
-          z1 += b;
+          float a, b;
+          unpair(fma2(pair(s[32 * e + 2 * j], s[32 * e + 2 * j + 1]), scale2, f2), a, b);
+          a = exp2_fast(a);
+          b = exp2_fast(b);
+          z[j & 1] = add2(z[j & 1], pair(a, b));
           w[j] = bf16_pair(a, b);
         }
         tmem_st16(s_at + 16 * e, w);
+        if (e & 1) {  // half of the tokens: their product can begin
+          wait_st();
+          fence_before();
+          mbar_arrive(&sm.p_full[t][e >> 1]);
+        }
       }
+      float z0, z1;
+      unpair(add2(z[0], z[1]), z0, z1);
       l += z0 + z1;
-      wait_st();
-      fence_before();
-      mbar_arrive(&sm.p_full[t]);
     }
     // ---------------- the row's output ----------------
     float o[kD];

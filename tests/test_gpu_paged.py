@@ -172,6 +172,20 @@ def test_decode_splits(kvs, R, G, n_):
     ref.check_decode(out, lse, q, k, v, table, lens, 0, 0, SC, torch.zeros_like(mass), mass)
 
 
+@pytest.mark.parametrize("H", [1, 2, 3, 5, 6, 7, 8])
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("qdt", [torch.bfloat16, torch.float32])
+def test_decode_splits_head_counts(kvs, H, weights, qdt):
+    """Rows cut into many parts, and into few, with every head count."""
+    lens = [12000, 30011, 2570, 64]
+    k, v, table, n = ref.make(lens, 2, 64, seed=H, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(4, 2, H, D, device=DEV).to(qdt)
+    mass = torch.zeros(4, 2, cache.cap, device=DEV) if weights else None
+    out, lse = kvs.paged_decode_attn(q, cache, mass=mass)
+    ref.check_decode(out, lse, q, k, v, table, lens, 0, 0, SC, torch.zeros_like(mass) if weights else None, mass)
+
+
 def test_decode_extreme_logits(kvs):
     """Logits from -3e4 to 3e4 and equal ones: the running maximum carries every one."""
     lens = [700, 700]
