@@ -53,7 +53,8 @@ struct PromptSmem {
   alignas(1024) unsigned char q[2][kTileBytes];
   unsigned char k[kStages][kTileBytes];
   unsigned char v[kStages][kTileBytes];
-  uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_clean[kStages], v_empty[kStages];
+  uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t v_clean;  // a phase for each tile that had rows to clear
   uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full by tile and half of the tokens
   int groups[kInfos];  // by tile: which 16-token groups were loaded
   uint32_t tmem;
@@ -111,6 +112,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 // Arrives on bar when every product issued so far is done.
 __device__ __forceinline__ void mma_commit_to(uint64_t* bar) {
@@ -250,21 +257,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
     }
   }
   const int tiles = nsink + (end + kTok - 1) / kTok - first;
+  // whether a tile of V has rows to clear
+  auto ragged = [&](int t0, int there) {
+    return there != 0xFF || t0 + kTok > end || (t0 < lo && t0 + kTok > p.sinks);
+  };
   auto tile_token = [&](int i) { return (i < nsink ? i : first + i - nsink) * kTok; };
 
   if (tid == 0) {
-    mbar_init(&sm.q_full, 32 * kSoftWarps);
+    mbar_init(&sm.q_full, kSoftWarps);
+    mbar_init(&sm.v_clean, 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sm.k_full[i], 1);
       mbar_init(&sm.k_empty[i], 1);
       mbar_init(&sm.v_full[i], 1);
-      mbar_init(&sm.v_clean[i], 1);
       mbar_init(&sm.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i][0], kRows);
-      mbar_init(&sm.p_full[i][1], kRows);
+      mbar_init(&sm.p_full[i][0], kRows / 32);
+      mbar_init(&sm.p_full[i][1], kRows / 32);
       mbar_init(&sm.o_full[i], 1);
     }
     sm.abort_flag = 0;
@@ -298,17 +309,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
       const int box = min(1 << kv.shift, kTok), pages = kTok / box;
       const int half = lane & 1, sub = lane >> 1;
       int issued = 0;
-      // this lane's page of tile i
-      auto look = [&](int i) {
+      // this lane's page id of tile i, unchecked (nothing waits for it here); -1 where none is needed
+      auto wanted = [&](int i) {
         const int t = tile_token(i) + sub * box;
-        if (sub >= pages || t >= end || (t >= p.sinks && t + box <= lo)) return -1;
-        return kv.page_of(r, t, p.dev_status);
+        return sub < pages && t < end && (t < p.sinks || t + box > lo);
       };
+      const int32_t* table = kv.table + r * kv.table_ld;
+      auto look = [&](int i) { return wanted(i) ? __ldg(table + ((tile_token(i) + sub * box) >> kv.shift)) : -1; };
       int next = tiles > 0 ? look(0) : -1;
       for (int i = 0; i < tiles; ++i) {
         const int st = i % kStages;
-        const int id = next;
+        int id = next;
         if (i + 1 < tiles) next = look(i + 1);
+        if (static_cast<unsigned>(id) >= static_cast<unsigned>(kv.num_pages)) {
+          if (wanted(i)) set_status(p.dev_status, KVS_EBOUNDS);
+          id = -1;
+        }
         const unsigned have = __ballot_sync(0xFFFFFFFFu, id >= 0);
         const int in_page = (tile_token(i) + sub * box) & ((1 << kv.shift) - 1);
         const uint32_t at = half * kHalfBytes + sub * box * 128;
@@ -351,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
         if (lane == 0) ok = wait(&sm.v_full[st], (i / kStages) & 1);
         if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
         const int t0 = tile_token(i), there = sm.groups[i % kInfos];
-        if (there != 0xFF || t0 + kTok > end || (t0 < lo && t0 + kTok > p.sinks)) {
+        if (ragged(t0, there)) {
           for (int x = lane; x < kTok * 16; x += 32) {
             const int row = x >> 4, t = t0 + row;
             if ((there >> (row >> 4) & 1) && t < end && (t >= lo || t < p.sinks)) continue;
@@ -360,60 +376,76 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
           }
           asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
           __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.v_clean);
         }
-        if (lane == 0) mbar_arrive(&sm.v_clean[st]);
       }
     } else if (warp == kMmaWarp) {
       // ---------------- products ----------------
-      if (lane == 0 && tiles > 0) {
+      // (the whole warp goes through the loop, so that descriptors stay in
+      // uniform registers; one lane issues)
+      if (tiles > 0) {
         const uint64_t dq = desc_k_major(sm_addr(sm.q[0])), dk = desc_k_major(sm_addr(sm.k[0])),
                        dv = desc_mn_major(sm_addr(sm.v[0]));
+        const bool leader = elect_one();
         auto qk = [&](int t, int i) {
+          const uint64_t a = dq + t * (kTileBytes >> 4), b = dk + (i % kStages) * (kTileBytes >> 4);
+          const uint32_t d = tmem + 128 * t;
+          if (leader) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const uint64_t step = (ks >> 2) * (kHalfBytes >> 4) + (ks & 3) * 2;
-            mma_ss(tmem + 128 * t, dq + t * (kTileBytes >> 4) + step, dk + (i % kStages) * (kTileBytes >> 4) + step, kIdesc,
-                   ks > 0);
+            for (int ks = 0; ks < 8; ++ks) {
+              const uint64_t step = (ks >> 2) * (kHalfBytes >> 4) + (ks & 3) * 2;
+              mma_ss(d, a + step, b + step, kIdesc, ks > 0);
+            }
+            mma_commit_to(&sm.s_full[t]);
           }
-          mma_commit_to(&sm.s_full[t]);
         };
-        bool ok = wait(&sm.q_full, 0) && wait(&sm.k_full[0], 0);
+        auto commit = [&](uint64_t* bar) {
+          if (leader) mma_commit_to(bar);
+        };
+        auto wait_all = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(b, parity)) != 0; };
+        int cleaned = 0;
+        bool ok = wait_all(&sm.q_full, 0) && wait_all(&sm.k_full[0], 0);
         if (ok) {
           fence_after();
           qk(0, 0);
           qk(1, 0);
-          mma_commit_to(&sm.k_empty[0]);
+          commit(&sm.k_empty[0]);
         }
         for (int i = 0; i < tiles && ok; ++i) {
           const int st = i % kStages;
+          ok = wait_all(&sm.v_full[st], (i / kStages) & 1);
+          if (ok && ragged(tile_token(i), sm.groups[i % kInfos])) ok = wait_all(&sm.v_clean, cleaned++ & 1);
           for (int t = 0; t < 2 && ok; ++t) {
-            if (t == 0) ok = wait(&sm.v_full[st], (i / kStages) & 1) && wait(&sm.v_clean[st], (i / kStages) & 1);
-            for (int e = 0; e < 2 && ok; ++e) {
-              ok = wait(&sm.p_full[t][e], i & 1);
+            const uint32_t d = tmem + 256 + 128 * t, a = tmem + 128 * t;
+            const uint64_t b = dv + st * (kTileBytes >> 4);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              ok = ok && wait_all(&sm.p_full[t][e], i & 1);
               if (!ok) break;
               fence_after();
+              if (leader) {
 #pragma unroll
-              for (int ks = 4 * e; ks < 4 * e + 4; ++ks)
-                mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * ks, dv + st * (kTileBytes >> 4) + ks * (2048 >> 4),
-                       kIdescMn, i > 0 || ks > 0);
+                for (int ks = 4 * e; ks < 4 * e + 4; ++ks)
+                  mma_ts(d, a + 8 * ks, b + ks * (2048 >> 4), kIdescMn, i > 0 || ks > 0);
+              }
             }
             if (!ok) break;
-            if (t == 1) mma_commit_to(&sm.v_empty[st]);
+            if (t == 1) commit(&sm.v_empty[st]);
             if (i + 1 == tiles) {
-              mma_commit_to(&sm.o_full[t]);
+              commit(&sm.o_full[t]);
               continue;
             }
             if (t == 0) {
-              ok = wait(&sm.k_full[(i + 1) % kStages], ((i + 1) / kStages) & 1);
+              ok = wait_all(&sm.k_full[(i + 1) % kStages], ((i + 1) / kStages) & 1);
               if (!ok) break;
               fence_after();
             }
             qk(t, i + 1);
-            if (t == 1) mma_commit_to(&sm.k_empty[(i + 1) % kStages]);
+            if (t == 1) commit(&sm.k_empty[(i + 1) % kStages]);
           }
         }
         if (!ok) {  // products already issued end before the block does
-          mma_commit_to(&sm.o_full[0]);
+          commit(&sm.o_full[0]);
           mbar_wait(&sm.o_full[0], 0);
         }
       }
@@ -426,22 +458,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + 256 + 128 * t;
     const float ninf = -__int_as_float(0x7f800000);
-    // the queries, half a warp to a row
-    for (int x = 0; x < 16; ++x) {
-      const int rr = 32 * (warp & 3) + 2 * x + (lane >> 4), row = 128 * t + rr, ch = lane & 15;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (row < rows) {
-        const int at = row0 + row;
-        v = __ldg(reinterpret_cast<const uint4*>(p.q + (q0 + at / H) * p.q_ld + (g * H + at % H) * kD + 8 * ch));
-        v.x ^= p.flip;
-        v.y ^= p.flip;
-        v.z ^= p.flip;
-        v.w ^= p.flip;
+    // the queries, half a warp to a row, eight loads in flight
+    const int w0 = 32 * (warp & 3), ch = lane & 15;
+    auto row_of = [&](int rr, int64_t ld) {  // element offset of row rr of the tile
+      const int at = row0 + 128 * t + rr, tok = at / H;
+      return (q0 + tok) * ld + (g * H + at - tok * H) * kD;
+    };
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint4 v[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int rr = w0 + 16 * half + 2 * x + (lane >> 4);
+        v[x] = make_uint4(0, 0, 0, 0);
+        if (128 * t + rr < rows) v[x] = __ldg(reinterpret_cast<const uint4*>(p.q + row_of(rr, p.q_ld) + 8 * ch));
       }
-      *reinterpret_cast<uint4*>(sm.q[t] + (ch >> 3) * kHalfBytes + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int rr = w0 + 16 * half + 2 * x + (lane >> 4);
+        v[x].x ^= p.flip;
+        v[x].y ^= p.flip;
+        v[x].z ^= p.flip;
+        v[x].w ^= p.flip;
+        *reinterpret_cast<uint4*>(sm.q[t] + (ch >> 3) * kHalfBytes + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v[x];
+      }
     }
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-    mbar_arrive(&sm.q_full);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.q_full);
 
     const int at = row0 + min(mine, rows - 1);
     const int pos = n - c + at / H;
@@ -451,14 +495,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
     float m = ninf, l = 0.f;
     bool ok = true;
     for (int i = 0; i < tiles; ++i) {
-      int got = 1;
-      if (lane == 0) got = wait(&sm.s_full[t], i & 1);
-      got = __shfl_sync(0xFFFFFFFFu, got, 0);
-      if (!got) {
+      if (!__all_sync(0xFFFFFFFFu, wait(&sm.s_full[t], i & 1))) {
         ok = false;
         break;
       }
-      __syncwarp();
       fence_after();
       float s[kTok];
 #pragma unroll
@@ -525,40 +565,44 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
         if (e & 1) {  // half of the tokens: their product can begin
           wait_st();
           fence_before();
-          mbar_arrive(&sm.p_full[t][e >> 1]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_full[t][e >> 1]);
         }
       }
       float z0, z1;
       unpair(add2(z[0], z[1]), z0, z1);
       l += z0 + z1;
     }
-    // ---------------- the row's output ----------------
+    // ---------------- the rows' output ----------------
     float o[kD];
 #pragma unroll
     for (int j = 0; j < kD; ++j) o[j] = 0.f;
-    if (ok && tiles > 0) {
-      int got = 1;
-      if (lane == 0) got = wait(&sm.o_full[t], 0);
-      got = __shfl_sync(0xFFFFFFFFu, got, 0);
-      __syncwarp();
-      if (got) {
-        fence_after();
+    if (ok && tiles > 0 && __all_sync(0xFFFFFFFFu, wait(&sm.o_full[t], 0))) {
+      fence_after();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) tmem_ld32(o_at + 32 * e, o + 32 * e);
-        wait_ld();
-      }
+      for (int e = 0; e < 4; ++e) tmem_ld32(o_at + 32 * e, o + 32 * e);
+      wait_ld();
     }
-    if (mine < rows) {
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-      uint16_t* to = p.out + (q0 + at / H) * p.out_ld + (g * H + at % H) * kD;
+    // through this warp's rows of the queries, which no product reads any more
+    // (rounded to bf16 here), so that half a warp writes a row
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    unsigned char* rows_at = sm.q[t] + w0 * 128;
 #pragma unroll
-      for (int j = 0; j < kD; j += 8)
-        *reinterpret_cast<uint4*>(to + j) =
-            make_uint4(bf16_pair(o[j] * inv, o[j + 1] * inv), bf16_pair(o[j + 2] * inv, o[j + 3] * inv),
-                       bf16_pair(o[j + 4] * inv, o[j + 5] * inv), bf16_pair(o[j + 6] * inv, o[j + 7] * inv));
-      if (p.lse)
-        p.lse[static_cast<size_t>(q0 + at / H) * G * H + g * H + at % H] =
-            l == 0.f ? ninf : (m + log2f(l)) * 0.6931471805599453f;
+    for (int j = 0; j < 16; ++j)
+      *reinterpret_cast<uint4*>(rows_at + (j >> 3) * kHalfBytes + lane * 128 + (((j & 7) ^ (lane & 7)) << 4)) =
+          make_uint4(bf16_pair(o[8 * j] * inv, o[8 * j + 1] * inv), bf16_pair(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
+                     bf16_pair(o[8 * j + 4] * inv, o[8 * j + 5] * inv),
+                     bf16_pair(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
+    if (mine < rows && p.lse)
+      p.lse[static_cast<size_t>(q0 + at / H) * G * H + g * H + at % H] =
+          l == 0.f ? ninf : (m + log2f(l)) * 0.6931471805599453f;
+    __syncwarp();
+#pragma unroll 4
+    for (int x = 0; x < 16; ++x) {
+      const int rr = 2 * x + (lane >> 4);
+      if (128 * t + w0 + rr < rows)
+        *reinterpret_cast<uint4*>(p.out + row_of(w0 + rr, p.out_ld) + 8 * ch) =
+            *reinterpret_cast<const uint4*>(rows_at + (ch >> 3) * kHalfBytes + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
     }
   }
   fence_before();
