@@ -458,24 +458,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + 256 + 128 * t;
     const float ninf = -__int_as_float(0x7f800000);
-    // the queries, half a warp to a row, eight loads in flight
+    // the queries, half a warp to a row, sixteen loads in flight
     const int w0 = 32 * (warp & 3), ch = lane & 15;
-    auto row_of = [&](int rr, int64_t ld) {  // element offset of row rr of the tile
-      const int at = row0 + 128 * t + rr, tok = at / H;
-      return (q0 + tok) * ld + (g * H + at - tok * H) * kD;
+    // row x of the block is head v % H of token tok0 + v / H, v = row0 % H + x
+    // (v < 264: the division by H is a multiplication)
+    const int tok0 = row0 / H, rem = row0 - tok0 * H;
+    const uint32_t by_h = 65536u / H + 1;
+    auto token_of = [&](int x) { return static_cast<int>((rem + x) * by_h >> 16); };
+    auto row_of = [&](int x, int64_t ld) {  // element offset of the row
+      const int tk = token_of(x);
+      return (q0 + tok0 + tk) * ld + (g * H + rem + x - tk * H) * kD;
     };
+    {
+      uint4 v[16];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint4 v[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const int rr = w0 + 16 * half + 2 * x + (lane >> 4);
+      for (int x = 0; x < 16; ++x) {
+        const int rr = 128 * t + w0 + 2 * x + (lane >> 4);
         v[x] = make_uint4(0, 0, 0, 0);
-        if (128 * t + rr < rows) v[x] = __ldg(reinterpret_cast<const uint4*>(p.q + row_of(rr, p.q_ld) + 8 * ch));
+        if (rr < rows) v[x] = __ldg(reinterpret_cast<const uint4*>(p.q + row_of(rr, p.q_ld) + 8 * ch));
       }
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const int rr = w0 + 16 * half + 2 * x + (lane >> 4);
+      for (int x = 0; x < 16; ++x) {
+        const int rr = w0 + 2 * x + (lane >> 4);
         v[x].x ^= p.flip;
         v[x].y ^= p.flip;
         v[x].z ^= p.flip;
@@ -487,11 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.q_full);
 
-    const int at = row0 + min(mine, rows - 1);
-    const int pos = n - c + at / H;
-    // what every row of this warp sees: [w_all, p_all], and none sees more than p_any
-    const int p_first = n - c + (row0 + min(128 * t + 32 * (warp & 3), rows - 1)) / H;
-    const int p_last = n - c + (row0 + min(128 * t + 32 * (warp & 3) + 31, rows - 1)) / H;
+    const int pos = p_lo + token_of(min(mine, rows - 1));
+    // the first and last position of this warp's rows
+    const int p_first = p_lo + token_of(min(128 * t + w0, rows - 1));
+    const int p_last = p_lo + token_of(min(128 * t + w0 + 31, rows - 1));
     float m = ninf, l = 0.f;
     bool ok = true;
     for (int i = 0; i < tiles; ++i) {
@@ -574,34 +577,37 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
       l += z0 + z1;
     }
     // ---------------- the rows' output ----------------
-    float o[kD];
-#pragma unroll
-    for (int j = 0; j < kD; ++j) o[j] = 0.f;
-    if (ok && tiles > 0 && __all_sync(0xFFFFFFFFu, wait(&sm.o_full[t], 0))) {
-      fence_after();
-#pragma unroll
-      for (int e = 0; e < 4; ++e) tmem_ld32(o_at + 32 * e, o + 32 * e);
-      wait_ld();
-    }
     // through this warp's rows of the queries, which no product reads any more
-    // (rounded to bf16 here), so that half a warp writes a row
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    // (rounded to bf16 here), so that half a warp writes a row. (Loops that are
+    // not unrolled: code that runs once a block is fetched once a block.)
+    const bool done = ok && tiles > 0 && __all_sync(0xFFFFFFFFu, wait(&sm.o_full[t], 0));
+    fence_after();
+    const float inv = !done ? 0.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
     unsigned char* rows_at = sm.q[t] + w0 * 128;
+#pragma unroll 1
+    for (int e = 0; e < 4; ++e) {
+      float o[32];
+      tmem_ld32(o_at + 32 * e, o);
+      wait_ld();
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      *reinterpret_cast<uint4*>(rows_at + (j >> 3) * kHalfBytes + lane * 128 + (((j & 7) ^ (lane & 7)) << 4)) =
-          make_uint4(bf16_pair(o[8 * j] * inv, o[8 * j + 1] * inv), bf16_pair(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
-                     bf16_pair(o[8 * j + 4] * inv, o[8 * j + 5] * inv),
-                     bf16_pair(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
+      for (int j = 0; j < 4; ++j) {
+        uint4 v = make_uint4(bf16_pair(o[8 * j] * inv, o[8 * j + 1] * inv), bf16_pair(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
+                             bf16_pair(o[8 * j + 4] * inv, o[8 * j + 5] * inv),
+                             bf16_pair(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
+        if (!done) v = make_uint4(0, 0, 0, 0);  // tensor memory that nothing was written to
+        *reinterpret_cast<uint4*>(rows_at + (e >> 1) * kHalfBytes + lane * 128 +
+                                  (((4 * (e & 1) + j) ^ (lane & 7)) << 4)) = v;
+      }
+    }
     if (mine < rows && p.lse)
-      p.lse[static_cast<size_t>(q0 + at / H) * G * H + g * H + at % H] =
+      p.lse[row_of(mine, static_cast<int64_t>(G) * H * kD) / kD] =
           l == 0.f ? ninf : (m + log2f(l)) * 0.6931471805599453f;
     __syncwarp();
 #pragma unroll 4
     for (int x = 0; x < 16; ++x) {
       const int rr = 2 * x + (lane >> 4);
       if (128 * t + w0 + rr < rows)
-        *reinterpret_cast<uint4*>(p.out + row_of(w0 + rr, p.out_ld) + 8 * ch) =
+        *reinterpret_cast<uint4*>(p.out + row_of(128 * t + w0 + rr, p.out_ld) + 8 * ch) =
             *reinterpret_cast<const uint4*>(rows_at + (ch >> 3) * kHalfBytes + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
     }
   }
