@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
       mbar_init(&sm.k_full[i], 1);
       mbar_init(&sm.k_empty[i], 1);
       mbar_init(&sm.v_full[i], 1);
-      mbar_init(&sm.v_empty[i], 1);
+      mbar_init(&sm.v_empty[i], 2);  // the products that read it, and the clearing warp
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
@@ -378,6 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.v_clean);
         }
+        // the slot is not filled again before this warp has passed it: it must
+        // not fall two phases of v_full behind
+        if (lane == 0) mbar_arrive(&sm.v_empty[st]);
       }
     } else if (warp == kMmaWarp) {
       // ---------------- products ----------------
