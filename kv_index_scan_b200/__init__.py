@@ -572,19 +572,30 @@ def _on(dev: torch.device, stream):
     return torch.cuda.device(dev)
 
 
+def _raw_stream(dev: torch.device) -> int:
+    """The current stream of dev, as its handle (torch.cuda.current_stream builds an object around it)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _need(name: str, t, shape, dtype, dev):
-    """t is a contiguous tensor of this shape and type on dev."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.device != dev \
-            or not t.is_contiguous():
+    """t, if it is a contiguous tensor of this shape and type on dev."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
         what = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else repr(type(t))
         raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {dev}, got {what}")
     return t
 
 
+def _check_ws(ws, dev):
+    if not (ws.device == dev and ws.dtype is torch.uint8 and ws.is_contiguous()):
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
+
+
 def _counts(**values):
     """Every value fits the C boundary's int32 and is not negative."""
     for name, v in values.items():
-        _require(isinstance(v, int) and 0 <= v < 2 ** 31, f"{name} must be an int from 0 to 2^31 - 1, got {v!r}")
+        if not (isinstance(v, int) and 0 <= v < 2147483648):
+            raise ValueError(f"{name} must be an int from 0 to 2^31 - 1, got {v!r}")
 
 
 class PagedKV:
@@ -617,9 +628,18 @@ class PagedKV:
                            table.stride(0) if self.R > 1 else self.max_pages, n.data_ptr(), self.R, self.G, self.D,
                            self.page, self.max_pages, self.num_pages)
         self._ref = ctypes.pointer(self._c)
+        self._state_shape = torch.Size((self.R, self.G, self.cap))
+        self._r_shape, self._cu_shape = torch.Size((self.R,)), torch.Size((self.R + 1,))
+        self._ws_bytes = {}  # what the library asks for, by call and sizes
 
     def _state(self, name, t, dtype):
-        return None if t is None else _need(name, t, (self.R, self.G, self.cap), dtype, self.device).data_ptr()
+        return None if t is None else _need(name, t, self._state_shape, dtype, self.device).data_ptr()
+
+    def _workspace(self, query, *sizes) -> torch.Tensor:
+        nb = self._ws_bytes.get((query, sizes))
+        if nb is None:
+            nb = self._ws_bytes[query, sizes] = max(int(getattr(_lib, query)(self.R, self.G, *sizes)), 16)
+        return torch.empty(nb, dtype=torch.uint8, device=self.device)
 
 
 def paged_append(cache: PagedKV, Knew: torch.Tensor, Vnew: torch.Tensor, cu=None, mass=None, pos=None, seen=None,
@@ -628,28 +648,30 @@ def paged_append(cache: PagedKV, Knew: torch.Tensor, Vnew: torch.Tensor, cu=None
     packed by request with cu int32 [R+1] (None: one token each). cache.n already counts them. mass f32 and
     pos int32 [R][G][cap] get 0 and the token's place (counted by seen int32 [R])."""
     dev = cache.device
-    _require(Knew.dim() == 3 and Knew.shape == Vnew.shape and Knew.shape[1:] == (cache.G, cache.D)
-             and Knew.dtype == Vnew.dtype == torch.bfloat16 and Knew.device == Vnew.device == dev,
-             f"Knew and Vnew must be bf16 [T][{cache.G}][{cache.D}] on {dev}")
+    shape = Knew.shape
+    if not (len(shape) == 3 and Vnew.shape == shape and shape[1] == cache.G and shape[2] == cache.D
+            and Knew.dtype is torch.bfloat16 and Vnew.dtype is torch.bfloat16 and Knew.device == dev
+            and Vnew.device == dev):
+        raise ValueError(f"Knew and Vnew must be bf16 [T][{cache.G}][{cache.D}] on {dev}")
     st = Knew.stride()
     _require(Vnew.stride() == st and st[2] == 1 and (st[1] == cache.D or cache.G == 1),
              "Knew and Vnew must have the same strides, their heads contiguous")
-    T = Knew.shape[0]
+    T = shape[0]
     ld = st[0] if T > 1 else cache.G * cache.D
-    cup = None if cu is None else _need("cu", cu, (cache.R + 1,), torch.int32, dev).data_ptr()
-    sp = None if seen is None else _need("seen", seen, (cache.R,), torch.int32, dev).data_ptr()
+    cup = None if cu is None else _need("cu", cu, cache._cu_shape, torch.int32, dev).data_ptr()
+    sp = None if seen is None else _need("seen", seen, cache._r_shape, torch.int32, dev).data_ptr()
     mp, pp = cache._state("mass", mass, torch.float32), cache._state("pos", pos, torch.int32)
     with _on(dev, stream):
         _check(_lib.kvs_paged_append(cache._ref, Knew.data_ptr(), Vnew.data_ptr(), ld, cup, T, mp, pp, sp,
-                                     _ptr(dev_status), torch.cuda.current_stream(dev).cuda_stream),
+                                     _ptr(dev_status), _raw_stream(dev)),
                "kvs_paged_append")
 
 
 def paged_decode_workspace(cache: PagedKV, H: int, weights: bool = False) -> torch.Tensor:
     """A workspace for paged_decode_attn, for callers that keep one (calls that may run at the same time
     need one each)."""
-    nb = _lib.kvs_paged_decode_workspace_size(cache.R, cache.G, H, cache.cap if weights else 0)
-    return torch.empty(max(int(nb), 16), dtype=torch.uint8, device=cache.device)
+    with _on(cache.device, None):
+        return cache._workspace("kvs_paged_decode_workspace_size", H, cache.cap if weights else 0)
 
 
 def paged_decode_attn(q: torch.Tensor, cache: PagedKV, window: int = 0, sinks: int = 0, scale: float | None = None,
@@ -679,13 +701,12 @@ def paged_decode_attn(q: torch.Tensor, cache: PagedKV, window: int = 0, sinks: i
         if ws is None:
             ws = paged_decode_workspace(cache, H, mass is not None)
         else:
-            _require(ws.device == dev and ws.dtype == torch.uint8 and ws.is_contiguous(),
-                     f"ws must be a contiguous uint8 tensor on {dev}")
+            _check_ws(ws, dev)
         a = PagedDecodeArgsC(cache._ref, q.data_ptr(), KVS_BF16 if qd == torch.bfloat16 else KVS_F32, H, window,
                              sinks, 1.0 / math.sqrt(cache.D) if scale is None else scale, out.data_ptr(),
                              lse.data_ptr(), mp, mo)
         _check(_lib.paged_decode_attn(ctypes.byref(a), ws.data_ptr(), ws.numel(), _ptr(dev_status),
-                                      torch.cuda.current_stream(dev).cuda_stream), "paged_decode_attn")
+                                      _raw_stream(dev)), "paged_decode_attn")
     return out, lse
 
 
@@ -696,27 +717,30 @@ def paged_prompt_attn(q: torch.Tensor, cu: torch.Tensor, cache: PagedKV, window:
     itself and the window - 1 before it, and the first `sinks`. Rows from cu[R] on are left as they are
     (zero in an `out` and `lse` made here)."""
     dev = cache.device
-    _require(q.dim() == 3 and q.dtype == torch.bfloat16 and q.device == dev and q.shape[2] == cache.D
-             and q.shape[1] % cache.G == 0, f"q must be bf16 [T][{cache.G}*H][{cache.D}] on {dev}")
     _counts(window=window, sinks=sinks)
-    T, Hq, D = q.shape
-    _need("cu", cu, (cache.R + 1,), torch.int32, dev)
+    shape = q.shape
+    if not (len(shape) == 3 and q.dtype is torch.bfloat16 and q.device == dev and shape[2] == cache.D
+            and shape[1] % cache.G == 0):
+        raise ValueError(f"q must be bf16 [T][{cache.G}*H][{cache.D}] on {dev}")
+    T, Hq, D = shape
+    _need("cu", cu, cache._cu_shape, torch.int32, dev)
     with _on(dev, stream):
         if out is None:
             out = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device=dev)
         else:
-            _require(out.shape == q.shape and out.dtype == torch.bfloat16 and out.device == dev,
-                     f"out must be bf16 {tuple(q.shape)} on {dev}")
-        for name, t in (("q", q), ("out", out)):
-            _require(t.stride(2) == 1 and (t.stride(1) == D or Hq == 1), f"{name} must have contiguous heads")
+            if not (out.shape == shape and out.dtype is torch.bfloat16 and out.device == dev):
+                raise ValueError(f"out must be bf16 {tuple(shape)} on {dev}")
+        qs, os_ = q.stride(), out.stride()
+        if not (qs[2] == 1 and os_[2] == 1 and (Hq == 1 or (qs[1] == D and os_[1] == D))):
+            raise ValueError("q and out must have contiguous heads")
         if lse is None:
             lse = torch.zeros(T, Hq, dtype=torch.float32, device=dev)
         else:
             _need("lse", lse, (T, Hq), torch.float32, dev)
-        ld = (q.stride(0), out.stride(0)) if T > 1 else (Hq * D, Hq * D)
+        ld = (qs[0], os_[0]) if T > 1 else (Hq * D, Hq * D)
         a = PagedPromptArgsC(cache._ref, q.data_ptr(), ld[0], cu.data_ptr(), T, Hq // cache.G, window, sinks,
                              1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), ld[1], lse.data_ptr())
-        _check(_lib.paged_prompt_attn(ctypes.byref(a), _ptr(dev_status), torch.cuda.current_stream(dev).cuda_stream),
+        _check(_lib.paged_prompt_attn(ctypes.byref(a), _ptr(dev_status), _raw_stream(dev)),
                "paged_prompt_attn")
     return out, lse
 
@@ -739,20 +763,18 @@ def paged_evict(cache: PagedKV, mass: torch.Tensor, budget: int, sinks: int = 0,
         pp = cache._state("pos", pos, torch.int32)
         _require(pp is not None or pos_out is None, "pos_out without pos")
         po = pp if pos_out is None else cache._state("pos_out", pos_out, torch.int32)
-        sp = None if seen is None else _need("seen", seen, (cache.R,), torch.int32, dev).data_ptr()
-        no = (cache.n if n_out is None else _need("n_out", n_out, (cache.R,), torch.int32, dev)).data_ptr()
+        sp = None if seen is None else _need("seen", seen, cache._r_shape, torch.int32, dev).data_ptr()
+        no = (cache.n if n_out is None else _need("n_out", n_out, cache._r_shape, torch.int32, dev)).data_ptr()
         _require(budget >= 1, "budget must be at least 1")
         if src is None:
             src = torch.empty(cache.R, cache.G, budget, dtype=torch.int32, device=dev)
         else:
             _need("src", src, (cache.R, cache.G, budget), torch.int32, dev)
         if ws is None:
-            nb = _lib.kvs_paged_evict_workspace_size(cache.R, cache.G, budget)
-            ws = torch.empty(max(int(nb), 16), dtype=torch.uint8, device=dev)
+            ws = cache._workspace("kvs_paged_evict_workspace_size", budget)
         else:
-            _require(ws.device == dev and ws.dtype == torch.uint8 and ws.is_contiguous(),
-                     f"ws must be a contiguous uint8 tensor on {dev}")
+            _check_ws(ws, dev)
         a = PagedEvictArgsC(cache._ref, mp, pp, sp, budget, sinks, recent, mo, po, no, src.data_ptr())
         _check(_lib.kvs_paged_evict(ctypes.byref(a), ws.data_ptr(), ws.numel(), _ptr(dev_status),
-                                    torch.cuda.current_stream(dev).cuda_stream), "kvs_paged_evict")
+                                    _raw_stream(dev)), "kvs_paged_evict")
     return src

@@ -40,6 +40,21 @@ struct PagedView {
 
 PagedView paged_view(const kvs_paged_kv* kv);
 
+// Allows `kernel` its dynamic shared memory on the current device, the first
+// time it is launched there (a launch pays for the call otherwise). Threads
+// that race here set the same value.
+template <auto kernel>
+void allow_smem(size_t bytes) {
+  static bool done[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && __atomic_load_n(&done[dev], __ATOMIC_RELAXED)) return;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) ==
+          cudaSuccess &&
+      dev >= 0 && dev < 64)
+    __atomic_store_n(&done[dev], true, __ATOMIC_RELAXED);
+}
+
 kvs_status paged_append_launch(const PagedView& kv, const uint16_t* Knew, const uint16_t* Vnew, int64_t new_ld,
                                const int32_t* cu, int T, float* mass, int32_t* pos, const int32_t* seen,
                                int32_t* dev_status, cudaStream_t s);

@@ -662,8 +662,7 @@ size_t carve(DecodeParams* p, void* ws, int R, int G, int H, int weight_cap) {
 
 template <bool kF32Q, bool kWeights>
 void launch(const DecodeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
-  cudaFuncSetAttribute(paged_decode_kernel<kF32Q, kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       static_cast<int>(sizeof(DecodeSmem)));
+  allow_smem<paged_decode_kernel<kF32Q, kWeights>>(sizeof(DecodeSmem));
   launch_chained(paged_decode_kernel<kF32Q, kWeights>, dim3(p.blocks), dim3(kThreads), sizeof(DecodeSmem), s, p, mk,
                  mv);
   const int chunks = kWeights ? (p.kv.max_pages * (1 << p.kv.shift) + kJoinTokens - 1) / kJoinTokens : 1;

@@ -318,8 +318,7 @@ kvs_status paged_evict_launch(const kvs_paged_evict_args* a, void* ws, int32_t* 
   const int64_t most = (cap + C - 1) / C;
   p.keys_room = static_cast<int>(most < kKeysMost ? most : kKeysMost);
   const size_t smem = static_cast<size_t>(p.keys_room) * sizeof(uint32_t);
-  cudaFuncSetAttribute(paged_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       kKeysMost * static_cast<int>(sizeof(uint32_t)));
+  allow_smem<paged_evict_kernel>(kKeysMost * sizeof(uint32_t));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(RG) * C);
   cfg.blockDim = dim3(kThreads);

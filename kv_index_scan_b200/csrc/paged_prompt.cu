@@ -650,8 +650,7 @@ kvs_status paged_prompt_launch(const kvs_paged_prompt_args* a, int32_t* dev_stat
   const int64_t part = a->T < p.kv.R ? a->T : p.kv.R;
   const int64_t grid = (whole + part) * p.kv.G;
   KVS_REQUIRE(grid < (1ll << 31), KVS_EUNSUPPORTED, "paged_prompt_attn: T=%d rows of G=%d heads", a->T, p.kv.G);
-  cudaFuncSetAttribute(paged_prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       static_cast<int>(sizeof(PromptSmem)));
+  allow_smem<paged_prompt_kernel>(sizeof(PromptSmem));
   launch_chained(paged_prompt_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), sizeof(PromptSmem), s, p, mk,
                  mv);
   return check_launch("paged_prompt_attn");
