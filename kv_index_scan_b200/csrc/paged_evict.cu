@@ -40,6 +40,11 @@ constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kKeysMost = 22 * 1024;  // keys of a block in shared memory (two blocks share an SM)
 constexpr int kFlight = 8;            // rows that a warp copies at a time
+constexpr int kRunLeast = 4096;       // slots of the longest row that a block takes at least
+constexpr int kBatch = 8;             // slots that a thread reads at a time
+
+constexpr uint32_t kSure = 0xFFFFFFFFu;  // key of a protected slot
+constexpr uint32_t kZero = 0x80000000u;  // of a weight of zero
 
 struct EvictParams {
   PagedView kv;
@@ -59,34 +64,34 @@ struct EvictParams {
 
 struct EvictShared {
   int hist[3][kBins];  // one a digit: no block clears what another still reads
-  unsigned long long part[kWarps];
+  unsigned long long part[2][kWarps];
+  int part32[3][kWarps];
   unsigned long long count;  // of this block, read by its cluster
-  int digit, need, equal;
+  int digit[3], need[3], equal[3];
 };
 
 // Sum over the block of v, and the sum of the threads before this one.
-__device__ __forceinline__ unsigned long long scan_block(unsigned long long v, unsigned long long* part,
-                                                         unsigned long long& total) {
+// (`part` may be written again after the block's next barrier.)
+template <typename T>
+__device__ __forceinline__ T scan_block(T v, T* part, T& total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  unsigned long long inc = v;
+  T inc = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+    const T y = __shfl_up_sync(0xFFFFFFFFu, inc, d);
     if (lane >= d) inc += y;
   }
   if (lane == 31) part[warp] = inc;
   __syncthreads();
-  const unsigned long long x = lane < kWarps ? part[lane] : 0ull;
-  unsigned long long w = x;
+  const T x = lane < kWarps ? part[lane] : T(0);
+  T w = x;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, w, d);
+  for (int d = 1; d < kWarps; d <<= 1) {
+    const T y = __shfl_up_sync(0xFFFFFFFFu, w, d);
     if (lane >= d) w += y;
   }
-  total = __shfl_sync(0xFFFFFFFFu, w, 31);
-  const unsigned long long before = __shfl_sync(0xFFFFFFFFu, w - x, warp);
-  __syncthreads();
-  return before + inc - v;
+  total = __shfl_sync(0xFFFFFFFFu, w, kWarps - 1);
+  return __shfl_sync(0xFFFFFFFFu, w - x, warp) + inc - v;
 }
 
 __global__ void __launch_bounds__(kThreads, 2) paged_evict_kernel(EvictParams p) {
@@ -95,6 +100,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_evict_kernel(EvictParams p)
   const cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto sync = [&] {
+    if (C == 1) __syncthreads();
+    else cluster.sync();
+  };
   for (int e = tid; e < 3 * kBins; e += kThreads) sm.hist[0][e] = 0;
   pdl_wait();
   pdl_trigger();
@@ -117,23 +126,34 @@ __global__ void __launch_bounds__(kThreads, 2) paged_evict_kernel(EvictParams p)
   const bool in_smem = per <= p.keys_room;
   auto key_of = [&](float m, int at) -> uint32_t {
     // protected ones above any weight, NaN below any
-    if (at < p.sinks || at >= seen - p.recent) return 0xFFFFFFFFu;
+    if (at < p.sinks || at >= seen - p.recent) return kSure;
     return m != m ? 0u : ordered_key(m);
   };
-#pragma unroll 4
-  for (int j = lo + tid; j < hi; j += kThreads) {
-    float m = 0.f;
-    int at = j;
-    if (j < n) {
-      m = mass[j];
-      if (pos) at = pos[j];
+  for (int j0 = lo + tid; j0 < hi; j0 += kBatch * kThreads) {
+    // loads of a batch before its stores, which may be to the same arrays
+    float m[kBatch];
+    int at[kBatch];
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const int j = j0 + x * kThreads;
+      m[x] = 0.f;
+      at[x] = j;
+      if (j < hi && j < n) {
+        m[x] = mass[j];
+        if (pos) at[x] = pos[j];
+      }
     }
-    if (j < b) {
-      src[j] = j < n ? j : -1;
-      if (j < n && mass_out != mass) mass_out[j] = m;
-      if (j < n && pos_out != pos) pos_out[j] = at;
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const int j = j0 + x * kThreads;
+      if (j >= hi) continue;
+      if (j < b) {
+        src[j] = j < n ? j : -1;
+        if (j < n && mass_out != mass) mass_out[j] = m[x];
+        if (j < n && pos_out != pos) pos_out[j] = at[x];
+      }
+      if (over && in_smem) evict_keys[j - lo] = key_of(m[x], at[x]);
     }
-    if (over && in_smem) evict_keys[j - lo] = key_of(m, at);
   }
   if (!over) return;  // (the whole cluster)
   auto key = [&](int j) { return in_smem ? evict_keys[j - lo] : key_of(mass[j], pos ? pos[j] : j); };
@@ -147,83 +167,94 @@ __global__ void __launch_bounds__(kThreads, 2) paged_evict_kernel(EvictParams p)
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = kShift[pass], width = pass == 2 ? 10 : 11;
     int* hist = sm.hist[pass];
-    for (int j0 = lo; j0 < hi; j0 += kThreads) {
-      const int j = j0 + tid;
-      const uint32_t k = j < hi ? key(j) : 0u;
-      const bool mine = j < hi && (pass == 0 || (k >> (shift + width)) == (cut >> (shift + width)));
-      // heavy bins are common (equal weights, the protected): one add for the
-      // lanes that share lane 0's bin, the others by themselves
-      const uint32_t d = (k >> shift) & ((1u << width) - 1u);
-      const unsigned act = __ballot_sync(0xFFFFFFFFu, mine);
-      if (act) {
-        const int lead = __ffs(act) - 1;
-        const uint32_t d0 = __shfl_sync(0xFFFFFFFFu, d, lead);
-        const unsigned same = __ballot_sync(0xFFFFFFFFu, mine && d == d0);
-        if (lane == lead) atomicAdd(&hist[d0], __popc(same));
-        else if (mine && d != d0) atomicAdd(&hist[d], 1);
+    // the protected (all in the first pass's top bin) and the weights of zero
+    // are many: each thread counts its own
+    int sure = 0, zero = 0;
+#pragma unroll 4
+    for (int j = lo + tid; j < hi; j += kThreads) {
+      const uint32_t k = key(j);
+      if (pass == 0 || (k >> (shift + width)) == (cut >> (shift + width))) {
+        if (k == kSure) ++sure;
+        else if (k == kZero) ++zero;
+        else atomicAdd(&hist[(k >> shift) & ((1u << width) - 1u)], 1);
       }
     }
-    cluster.sync();
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      sure += __shfl_xor_sync(0xFFFFFFFFu, sure, d);
+      zero += __shfl_xor_sync(0xFFFFFFFFu, zero, d);
+    }
+    if (lane == 0 && sure) atomicAdd(&hist[(kSure >> shift) & ((1u << width) - 1u)], sure);
+    if (lane == 0 && zero) atomicAdd(&hist[(kZero >> shift) & ((1u << width) - 1u)], zero);
+    sync();
     // bins from the top, kOwn a thread
     constexpr int kOwn = kBins / kThreads;
     static_assert(kOwn == 4, "a thread's bins are one 16-byte load");
     const int bin = kBins - kOwn * (tid + 1);
     int h[kOwn] = {0, 0, 0, 0};
-    for (int x = 0; x < C; ++x) {
-      const int4 v = *reinterpret_cast<const int4*>(cluster.map_shared_rank(hist, x) + bin);
+#pragma unroll
+    for (int x = 0; x < kMaxCluster; ++x) {
+      int4 v = make_int4(0, 0, 0, 0);
+      if (x < C) v = *reinterpret_cast<const int4*>((C == 1 ? hist : cluster.map_shared_rank(hist, x)) + bin);
       h[0] += v.x;
       h[1] += v.y;
       h[2] += v.z;
       h[3] += v.w;
     }
-    unsigned long long all;
-    int above = static_cast<int>(scan_block(static_cast<unsigned long long>(h[0] + h[1] + h[2] + h[3]), sm.part, all));
+    int all, above = scan_block(h[0] + h[1] + h[2] + h[3], sm.part32[pass], all);
 #pragma unroll
     for (int e = kOwn - 1; e >= 0; --e) {
       if (above < need && above + h[e] >= need) {
-        sm.digit = bin + e;
-        sm.need = need - above;
-        sm.equal = h[e];
+        sm.digit[pass] = bin + e;
+        sm.need[pass] = need - above;
+        sm.equal[pass] = h[e];
       }
       above += h[e];
     }
     __syncthreads();
-    cut |= static_cast<uint32_t>(sm.digit) << shift;
-    need = sm.need;
-    equal = sm.equal;
-    __syncthreads();
+    cut |= static_cast<uint32_t>(sm.digit[pass]) << shift;
+    need = sm.need[pass];
+    equal = sm.equal[pass];
+    if (equal == need) break;  // all of them: the lower digits need not be known
   }
 
   // this thread's piece of the block's run (an odd length: no bank conflicts)
   const int len = ((hi - lo + kThreads - 1) / kThreads) | 1;
   const int a0 = min(lo + tid * len, hi), a1 = min(a0 + len, hi);
   unsigned long long total;
-  auto before_us = [&](unsigned long long mine) {  // sums of the cluster's blocks before this one
+  // sums over the cluster's blocks before this one, and over all of them
+  auto before_us = [&](unsigned long long mine, unsigned long long& all) {
     if (tid == 0) sm.count = mine;
-    cluster.sync();
-    unsigned long long s = 0;
-    for (int x = 0; x < rank; ++x) s += *cluster.map_shared_rank(&sm.count, x);
-    return s;
+    sync();
+    unsigned long long v = lane < C ? *cluster.map_shared_rank(&sm.count, lane) : 0ull, w = lane < rank ? v : 0ull;
+#pragma unroll
+    for (int d = kMaxCluster / 2; d > 0; d >>= 1) {
+      v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+      w += __shfl_xor_sync(0xFFFFFFFFu, w, d);
+    }
+    all = __shfl_sync(0xFFFFFFFFu, v, 0);
+    return __shfl_sync(0xFFFFFFFFu, w, 0);
   };
+  unsigned long long last;  // holes and movers of the whole row
   int tie = 0;  // rank of the next tied key of this thread
   const bool some = equal > need;  // only some of the tied keys are kept
   if (some) {
     int t = 0;
     for (int j = a0; j < a1; ++j) t += key(j) == cut;
-    const unsigned long long mine = scan_block(t, sm.part, total);
-    tie = static_cast<int>(before_us(total) + mine);
-    cluster.sync();  // every block has read the counts
+    const unsigned long long mine = scan_block(static_cast<unsigned long long>(t), sm.part[0], total);
+    tie = static_cast<int>(before_us(total, last) + mine);
+    sync();  // every block has read the counts
   }
   const int tie0 = tie;
-  auto kept = [&](uint32_t k) { return k > cut || (k == cut && (!some || tie++ < need)); };
+  auto kept = [&](uint32_t k) { return some ? k > cut || (k == cut && tie++ < need) : k >= cut; };
   unsigned long long moves = 0;  // holes, and movers in the upper half
   for (int j = a0; j < a1; ++j) {
     const bool keep = kept(key(j));
     if (j < b) moves += keep ? 0ull : 1ull;
     else moves += keep ? 1ull << 32 : 0ull;
   }
-  unsigned long long at = scan_block(moves, sm.part, total);
-  at += before_us(total);
+  unsigned long long at = scan_block(moves, sm.part[1], total);
+  at += before_us(total, last);
   {
     int h = static_cast<int>(at & 0xFFFFFFFFull), m = static_cast<int>(at >> 32);
     int32_t* holes = p.holes + static_cast<size_t>(u) * b;
@@ -235,9 +266,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_evict_kernel(EvictParams p)
       if (j >= b && keep) movers[m++] = j;
     }
   }
-  unsigned long long last = 0;  // moves in all
-  for (int x = 0; x < C; ++x) last += *cluster.map_shared_rank(&sm.count, x);
-  cluster.sync();  // the lists are written, and every block has read the counts
+  sync();  // the lists are written, and every block has read the counts
   const int count = static_cast<int>(last & 0xFFFFFFFFull);
 
   // the moves, 32 a warp at a time
@@ -314,7 +343,7 @@ kvs_status paged_evict_launch(const kvs_paged_evict_args* a, void* ws, int32_t* 
   // thousand slots of the longest row there may be
   const int64_t cap = static_cast<int64_t>(a->kv->max_pages) * a->kv->page;
   int C = 1;
-  while (C < kMaxCluster && static_cast<int64_t>(RG) * C * 2 <= 2 * sm_count() && cap / (2 * C) >= 1024) C *= 2;
+  while (C < kMaxCluster && static_cast<int64_t>(RG) * C * 2 <= 2 * sm_count() && cap / (2 * C) >= kRunLeast) C *= 2;
   const int64_t most = (cap + C - 1) / C;
   p.keys_room = static_cast<int>(most < kKeysMost ? most : kKeysMost);
   const size_t smem = static_cast<size_t>(p.keys_room) * sizeof(uint32_t);
