@@ -61,6 +61,10 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
 kvs_status paged_tensor_map(CUtensorMap* map, const uint16_t* pool, const PagedView& kv, int rows, int halves,
                             const char* who);
 
+// The packed queries as a tensor [half][token][head][64 elements], with boxes of
+// a KV head's H heads and `tokens` tokens.
+kvs_status query_tensor_map(CUtensorMap* map, const kvs_paged_prompt_args* a, int tokens);
+
 // The tokens that a query at position p sees, as whole tiles of `kTile` tokens:
 // the sinks' tiles, then those from the window's first token to p. Tiles that
 // hold both are counted once.

@@ -3,6 +3,12 @@
 
 #include "internal.cuh"
 
+#define KVS_PROPAGATE(expr)                \
+  do {                                     \
+    const kvs_status st_ = (expr);         \
+    if (st_ != KVS_OK) return st_;         \
+  } while (0)
+
 namespace kvs {
 
 // kvs_paged_kv with the page size as a shift.

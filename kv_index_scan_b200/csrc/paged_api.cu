@@ -61,12 +61,6 @@ kvs_status check_mask(const char* who, int window, int sinks, float scale) {
   return KVS_OK;
 }
 
-#define KVS_PROPAGATE(expr)                \
-  do {                                     \
-    const kvs_status st_ = (expr);         \
-    if (st_ != KVS_OK) return st_;         \
-  } while (0)
-
 }  // namespace
 
 extern "C" {
