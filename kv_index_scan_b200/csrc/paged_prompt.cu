@@ -29,6 +29,12 @@
 //  * Two warps clear rows of V that no row of the block sees or that were not
 //    loaded (released or bad pages, behind the last token): their weights are
 //    zero, and zero times whatever lies there must not become NaN.
+// Measured: 8192 tokens of 32 heads over 8 KV heads, causal, 0.55 TFLOP: 0.44 to
+// 0.50 ms by the clocks that the power cap leaves (1.10 to 1.25 PFLOP/s; a large
+// library product reaches 1.66 in a burst and 1.40 for seconds); 2048 tokens over
+// 32768 with a window of 4096: 144 us (0.96 PFLOP/s; 256 items for 148 SMs); 128
+// tokens 10 us. The products with their loads alone take 0.32 and 0.09 ms: what
+// is left is each row tile's chain from S through the softmax to the next S.
 // Every wait is bounded; one that runs out writes KVS_ETIMEOUT, and the block
 // winds down with no copy in flight and its tensor memory freed.
 #include <cuda_bf16.h>

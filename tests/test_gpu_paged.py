@@ -323,6 +323,7 @@ def _prompt(kvs, lens, new, G, H, page, window, sinks, seed=0, pad=3, layout="he
     T = cu[-1] + pad
     g = torch.Generator(device=DEV).manual_seed(seed)
     q = torch.randn(T, G * H, D, generator=g, device=DEV).to(torch.bfloat16)
+    q[cu[-1]:] = float("nan")
     out = torch.full((T, G * H, D), 3.5, dtype=torch.bfloat16, device=DEV)
     lse = torch.full((T, G * H), -7.25, device=DEV)
     st = _status()
@@ -354,6 +355,69 @@ def test_prompt_lengths(kvs, lens, new):
 def test_prompt_long(kvs):
     _prompt(kvs, [4500], [4500], 1, 2, 64, 0, 0, seed=1)
     _prompt(kvs, [4500], [2000], 1, 2, 64, 1000, 4, seed=2)
+
+
+@pytest.mark.parametrize("G,H,window,sinks", [(4, 8, 0, 0), (3, 5, 300, 7), (8, 8, 64, 0)])
+def test_prompt_several_items_a_block(kvs, G, H, window, sinks):
+    """More items than SMs: a block takes items of several requests and KV heads in turn."""
+    _prompt(kvs, [1500, 1700, 3, 700], [1500, 900, 3, 640], G, H, 32, window, sinks, seed=G)
+
+
+def test_prompt_items_that_see_nothing(kvs):
+    """Many queries in front of the first token, between items that see something."""
+    lens, new, G, H = [3, 260, 0], [900, 260, 500], 8, 8
+    k, v, table, n = ref.make(lens, G, 16, seed=29)
+    cache = kvs.PagedKV(k, v, table, n)
+    cu = [0, 900, 1160, 1660]
+    q = torch.randn(1660, G * H, D, device=DEV).to(torch.bfloat16)
+    st = _status()
+    out, lse = kvs.paged_prompt_attn(q, torch.tensor(cu, dtype=torch.int32, device=DEV), cache, dev_status=st)
+    ref.check_prompt(out, lse, q, cu, k, v, table, lens, 0, 0, SC, G)
+    assert bool((out[:897] == 0).all()) and bool((out[1160:] == 0).all()) and int(st) == 0
+
+
+def test_empty_calls(kvs):
+    k, v, table, n = ref.make([20], 2, 16, seed=1)
+    cache = kvs.PagedKV(k, v, table, n)
+    cu = torch.zeros(2, dtype=torch.int32, device=DEV)
+    none = torch.empty(0, 8, D, dtype=torch.bfloat16, device=DEV)
+    out, lse = kvs.paged_prompt_attn(none, cu, cache)
+    assert out.shape == (0, 8, D) and lse.shape == (0, 8)
+    before = k.clone()
+    kvs.paged_append(cache, none[:, :2], none[:, :2], cu)
+    assert torch.equal(_bits(k), _bits(before))
+
+
+def test_calls_at_once_on_two_streams(kvs):
+    """Prompts, decodes and evictions of two caches side by side, again and again, give what they give alone."""
+    sides = []
+    for i in range(2):
+        k, v, table, n = ref.make([700 + 300 * i, 90, 2000], 4, 16, seed=40 + i, poison=False)
+        cache = kvs.PagedKV(k, v, table, n)
+        q = torch.randn(500, 16, D, device=DEV).to(torch.bfloat16)
+        cu = torch.tensor([0, 300, 350, 500], dtype=torch.int32, device=DEV)
+        mass = torch.rand(3, 4, cache.cap, device=DEV)
+        sides.append((cache, q, cu, q[:3].view(3, 4, 4, D).contiguous(), mass))
+
+    def run(i, stream):
+        cache, q, cu, q1, mass = sides[i]
+        mo, no = torch.zeros_like(mass), torch.zeros_like(cache.n)
+        return [*kvs.paged_prompt_attn(q, cu, cache, 200, 4, stream=stream), *kvs.paged_decode_attn(q1, cache, stream=stream),
+                kvs.paged_evict(cache, mass, 600, mass_out=mo, n_out=no, stream=stream)]
+
+    want = [run(i, None) for i in range(2)]  # (the moves of an eviction repeated are the same)
+    want = [run(i, None) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got.append((i, run(i, streams[i])))
+    torch.cuda.synchronize()
+    for i, outs in got:
+        for a, b in zip(outs, want[i]):
+            assert torch.equal(a, b)
 
 
 def test_prompt_many_requests(kvs):
@@ -583,6 +647,12 @@ def test_evict_infinities_nan_and_signed_zero(kvs):
 
 def test_evict_long_rows(kvs):
     _evict_case(kvs, [70001, 52000, 9000], 1, 256, 8000, 4, 1000, 7, _rand(7), _none, None)
+
+
+def test_evict_rows_beyond_shared_memory(kvs):
+    """Runs of more slots than a block holds keys for."""
+    _evict_case(kvs, [190000, 188001], 1, 1024, 5000, 4, 1000, 17, _rand(17), _none, None)
+    _evict_case(kvs, [190000], 1, 1024, 70000, 4, 1000, 18, _rand(18, 50), _perm(18), None)
 
 
 def test_evict_many_rows(kvs):
