@@ -223,12 +223,12 @@ struct Item {
 // Item x of all, found by the whole warp: KV heads innermost, the blocks of a
 // request from its last (which sees most) to its first, the last request first.
 // False behind the last one.
-__device__ __forceinline__ bool find_item(const PromptParams& p, int64_t x, Item& it) {
+__device__ __forceinline__ bool find_item(const PromptParams& p, uint32_t x, Item& it) {
   const PagedView& kv = p.kv;
   const int lane = threadIdx.x & 31;
-  it.g = static_cast<int>(x % kv.G);
-  const int64_t order = x / kv.G;
-  int64_t base = 0;
+  const uint32_t order = x / static_cast<uint32_t>(kv.G);
+  it.g = static_cast<int>(x - order * kv.G);
+  uint32_t base = 0;
   for (int top = kv.R; top > 0; top -= 32) {
     const int r = top - 1 - lane;
     int q0 = 0, c = 0, n = 0;
@@ -237,11 +237,11 @@ __device__ __forceinline__ bool find_item(const PromptParams& p, int64_t x, Item
       c = max(0, p.start(r + 1) - q0);
       n = kv.length(r, p.dev_status);
     }
-    const int64_t mine = (c + 2 * p.per - 1) / (2 * p.per);
-    int64_t inc = mine;
+    const uint32_t mine = (static_cast<uint32_t>(c) + 2 * p.per - 1) / (2 * p.per);
+    uint32_t inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, d);
       if (lane >= d) inc += y;
     }
     const unsigned hit = __ballot_sync(0xFFFFFFFFu, order < base + inc);
@@ -285,9 +285,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
   // The block's items: one of each round of gridDim.x, in the order of the
   // blocks and in the reverse in turn (items shrink along the order). Every warp
   // finds them for itself.
-  int64_t round = 0;
+  uint32_t round = 0;
   auto next_item = [&](Item& it) {
-    const int64_t at = round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+    const uint32_t at = round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
     return find_item(p, round++ * gridDim.x + at, it);
   };
 
