@@ -41,7 +41,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kKeysMost = 22 * 1024;  // keys of a block in shared memory (two blocks share an SM)
-constexpr int kFlight = 8;            // rows that a warp copies at a time
+constexpr int kFlight = 4;            // rows that a warp copies at a time (8: registers spill, 82 us for 68)
 constexpr int kRunLeast = 4096;       // slots of the longest row that a block takes at least
 constexpr int kBatch = 8;             // slots that a thread reads at a time
 
@@ -164,10 +164,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_evict_kernel(EvictParams p)
   // the b-th largest key
   uint32_t cut = 0;
   int need = b, equal = 0;  // still to take among the keys that share the cut's digits, and how many do
-  constexpr int kShift[3] = {21, 10, 0};
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = kShift[pass], width = pass == 2 ? 10 : 11;
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), width = pass == 2 ? 10 : 11;
     int* hist = sm.hist[pass];
     // the protected (all in the first pass's top bin) and the weights of zero
     // are many: each thread counts its own
