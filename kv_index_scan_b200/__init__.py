@@ -1,6 +1,7 @@
 """Python binding of libkvscan.so: the B200 per-step top-k sparse-attention
 decode path (Fathom bit-plane index scan, top-k, hot-buffer gather, sparse GQA
-attention, and the lightning-indexer variant).
+attention, and the lightning-indexer variant), and beside it a paged K/V cache
+(PagedKV and the paged_* functions).
 
 This module only marshals arguments: it allocates output tensors with torch,
 passes raw device pointers and the current CUDA stream to the C ABI declared in
