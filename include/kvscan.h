@@ -453,7 +453,9 @@ KVS_API kvs_status decode_step_timed(const kvs_decode_args* a, void* ws, size_t 
  * read through: they may hold anything. An id outside 0 .. num_pages - 1 where
  * a row is needed writes KVS_EBOUNDS to dev_status, and the rows of that page
  * count as absent (not read, not written, not attended to).
- * Requests may share pages that no call writes.
+ * Requests may share pages that no call writes. Both attentions count by slot:
+ * once kvs_paged_evict has run, the slots of a request are in no order, and a
+ * window over them means nothing (window = 0 then).
  * ------------------------------------------------------------------------- */
 typedef struct {
   uint16_t* K; /* bf16; written by kvs_paged_append and kvs_paged_evict only */
@@ -523,10 +525,11 @@ KVS_API size_t kvs_paged_decode_workspace_size(int32_t R, int32_t G, int32_t H, 
  *   that sees nothing (p < 0) gets out = 0 and lse = -inf. Entries of cu
  *   outside 0 .. T are clamped (KVS_EBOUNDS).
  * The softmax and all sums are f32; the weights are rounded to bf16 for the
- * product with V, and out once at the end. A cached V row that is not finite
- * makes the outputs of queries not finite that see it, and may those of
- * queries up to 255 rows (token, head) before them; K and V rows that no
- * query of a 256-row block sees have no influence on it. No workspace. */
+ * product with V, and out once at the end. Queries are taken 2 * floor(128 / H)
+ * tokens at a time: a cached V row that is not finite makes the outputs of the
+ * queries that see it not finite, and may those of other queries taken with
+ * one that does; K and V rows that none of them sees have no influence on them.
+ * No workspace. */
 typedef struct {
   const kvs_paged_kv* kv;
   const uint16_t* q;

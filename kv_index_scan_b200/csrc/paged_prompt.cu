@@ -711,6 +711,16 @@ kvs_status paged_prompt_launch(const kvs_paged_prompt_args* a, int32_t* dev_stat
   // no more items than this, whatever the lengths: a part item a request, and whole ones
   const int64_t whole = a->T / (2 * p.per), part = a->T < p.kv.R ? a->T : p.kv.R;
   const int64_t items = (whole + part) * p.kv.G;
+  KVS_REQUIRE(items < (1ll << 31) - (1 << 20), KVS_EUNSUPPORTED, "paged_prompt_attn: T=%d queries of G=%d KV heads", a->T,
+              p.kv.G);
+  // the register split must fit what the kernel is launched with, or the softmax
+  // warps would wait for registers that never come
+  static const int regs = [] {
+    cudaFuncAttributes f{};
+    return cudaFuncGetAttributes(&f, paged_prompt_kernel) == cudaSuccess ? f.numRegs : 0;
+  }();
+  KVS_REQUIRE(regs * kThreads >= 32 * kSoftWarps * kSoftRegs + (kThreads - 32 * kSoftWarps) * kOtherRegs, KVS_ECUDA,
+              "paged_prompt_attn: built with %d registers a thread", regs);
   const int sms = sm_count();
   allow_smem<paged_prompt_kernel>(sizeof(PromptSmem));
   launch_chained(paged_prompt_kernel, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kThreads),
