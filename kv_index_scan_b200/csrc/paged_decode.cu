@@ -29,7 +29,7 @@
 //    log-sum-exp is known.
 // Measured: 16 requests of 16K to 128K tokens, 3.70 GB: 0.54 to 0.62 ms (5.99 to
 // 6.9 TB/s of the 6.55 a copy reaches); 32 requests seeing 4100 tokens each, 8
-// heads: 88 us (5.7 TB/s); one request of 4096 tokens: 12.6 us, 4.7 of them the join.
+// heads: 88 us (5.7 TB/s); one request of 4096 tokens: 11.1 us, 3 of them the join.
 #include <cuda_bf16.h>
 
 #include "async.cuh"
@@ -515,11 +515,149 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
 
 constexpr int kJoinThreads = 512;
 constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kFewBatch = 8;
 constexpr int kJoinTokens = 2048;  // tokens of a row that one block turns into weights
 
-// Row u's parts joined (block x = 0 of the row), and its weights (every block).
-// The lengths are read before the wait on the attention kernel: every block of
+// Parts way, way + ways, ... of a head, their maximum M, sum L and output acc
+// (four channels a lane) relative to it, kFewBatch of them loaded at a time.
+template <typename Part>
+__device__ __forceinline__ void join_parts(Part part, int way, int ways, int parts, int lane, float& M, float& L,
+                                           float4& acc) {
+  const float ninf = -__int_as_float(0x7f800000);
+  M = ninf;
+  L = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int x0 = way; x0 < parts; x0 += kFewBatch * ways) {
+    float2 ml[kFewBatch];
+    float4 v[kFewBatch];
+#pragma unroll
+    for (int e = 0; e < kFewBatch; ++e) {
+      const int x = x0 + e * ways;
+      ml[e] = make_float2(ninf, 0.f);
+      v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (x < parts) {
+        ml[e] = *reinterpret_cast<const float2*>(part(x));
+        v[e] = *reinterpret_cast<const float4*>(part(x) + 4 + 4 * lane);
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int e = 0; e < kFewBatch; ++e) top = fmaxf(top, ml[e].x);
+    const float f = top == ninf ? 0.f : top, a = exp2f(M - f);
+    M = top;
+    L *= a;
+    acc.x *= a;
+    acc.y *= a;
+    acc.z *= a;
+    acc.w *= a;
+#pragma unroll
+    for (int e = 0; e < kFewBatch; ++e) {
+      const float c = exp2f(ml[e].x - f);
+      L = fmaf(c, ml[e].y, L);
+      acc.x = fmaf(c, v[e].x, acc.x);
+      acc.y = fmaf(c, v[e].y, acc.y);
+      acc.z = fmaf(c, v[e].z, acc.z);
+      acc.w = fmaf(c, v[e].w, acc.w);
+    }
+  }
+}
+
+// Blocks b0 .. b1 hold parts of row u (r, g); the whole block works it out. The
+// lengths may be read before the wait on the attention kernel: every block of
 // that kernel had waited for whatever came before it when this one was let go.
+template <int kT>
+__device__ __forceinline__ void blocks_of_row(const DecodeParams& p, int r, int g, const VisibleTiles<kUnit>& vt,
+                                              int64_t (&scan_part)[2][kT / 32], int& b0, int& b1) {
+  const PagedView& kv = p.kv;
+  int64_t all = 0, before = 0;
+  for (int x = threadIdx.x; x < kv.R; x += kT) {
+    const int c = VisibleTiles<kUnit>(kv.length(x, nullptr), p.window, p.sinks).count;
+    all += c;
+    if (x < r) before += c;
+  }
+  int64_t U, base;
+  block_scan<kT>(all, scan_part[0], U);
+  block_scan<kT>(before, scan_part[1], base);
+  U *= kv.G;
+  base = base * kv.G + static_cast<int64_t>(g) * vt.count;
+  b0 = b1 = 0;
+  if (vt.count) {
+    const int nb = sharing(U, p.blocks);
+    b0 = block_of_unit(U, base, nb);
+    b1 = block_of_unit(U, base + vt.count - 1, nb);
+  }
+}
+
+// A row that nothing is seen of.
+__device__ __forceinline__ void write_nothing(const DecodeParams& p, int u) {
+  for (int e = threadIdx.x; e < p.H * kD; e += blockDim.x) p.out[static_cast<size_t>(u) * p.H * kD + e] = 0.f;
+  if (p.lse && threadIdx.x < p.H) p.lse[static_cast<size_t>(u) * p.H + threadIdx.x] = -__int_as_float(0x7f800000);
+}
+
+// Part x of head h of a row: block b0 + x's, in its second slot where the row begins.
+struct Parts {
+  const float* first;
+  int64_t slot;
+  __device__ __forceinline__ Parts(const DecodeParams& p, int b0, int h) {
+    slot = static_cast<int64_t>(p.H) * kPartRow;
+    first = p.part + (static_cast<int64_t>(b0) * kPartSlots + 1) * slot + h * kPartRow;
+  }
+  __device__ __forceinline__ const float* operator()(int x) const {
+    return x == 0 ? first : first - slot + x * kPartSlots * slot;
+  }
+};
+
+// Row u's parts joined, for no more rows than SMs (each then has many parts):
+// one round of loads, eight parts of a head in flight a warp, and the warps'
+// sums meet in shared memory. One row of 4096 tokens: the whole call 11.1 us,
+// 12.5 with the kernel below; 256 rows 90.4 us, 88.4 with the one below (its
+// registers leave room for one block an SM).
+__global__ void __launch_bounds__(kJoinThreads) paged_decode_join_few_kernel(const DecodeParams p) {
+  __shared__ int64_t scan_part[2][kJoinWarps];
+  __shared__ float s_sum[kJoinWarps][kD];
+  __shared__ float s_ml[kJoinWarps][2];
+  const float ninf = -__int_as_float(0x7f800000);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int u = blockIdx.x, r = u / p.kv.G, g = u % p.kv.G, H = p.H;
+  const VisibleTiles<kUnit> vt(p.kv.length(r, nullptr), p.window, p.sinks);
+  int b0, b1;
+  blocks_of_row<kJoinThreads>(p, r, g, vt, scan_part, b0, b1);
+  pdl_wait();
+  if (vt.count == 0) {
+    write_nothing(p, u);
+    return;
+  }
+  if (b0 == b1) return;
+  const int shift = H <= 1 ? 0 : (H <= 2 ? 1 : (H <= 4 ? 2 : 3)), heads = 1 << shift, ways = kJoinWarps >> shift;
+  const int h = warp & (heads - 1), way = warp >> shift;
+  if (h < H) {
+    float M, L;
+    float4 acc;
+    join_parts(Parts(p, b0, h), way, ways, b1 - b0 + 1, lane, M, L, acc);
+    if (lane == 0) {
+      s_ml[warp][0] = M;
+      s_ml[warp][1] = L;
+    }
+    *reinterpret_cast<float4*>(&s_sum[warp][4 * lane]) = acc;
+  }
+  __syncthreads();
+  for (int e = tid; e < H * kD; e += kJoinThreads) {
+    const int eh = e / kD;
+    float M = ninf, L = 0.f, o = 0.f;
+    for (int w = 0; w < ways; ++w) M = fmaxf(M, s_ml[w * heads + eh][0]);
+    const float f = M == ninf ? 0.f : M;
+    for (int w = 0; w < ways; ++w) {
+      const float c = exp2f(s_ml[w * heads + eh][0] - f);
+      L = fmaf(c, s_ml[w * heads + eh][1], L);
+      o = fmaf(c, s_sum[w * heads + eh][e % kD], o);
+    }
+    p.out[static_cast<size_t>(u) * H * kD + e] = o * (L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L));
+    if (p.lse && e % kD == 0)
+      p.lse[static_cast<size_t>(u) * H + eh] = L == 0.f ? ninf : (M + log2f(L)) * 0.6931471805599453f;
+  }
+}
+
+// Row u's parts joined (block x = 0 of the row), and its weights (every block).
 template <bool kWeights>
 __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const DecodeParams p, int chunks) {
   __shared__ int64_t scan_part[2][kJoinWarps];
@@ -532,44 +670,24 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const D
   const int r = u / kv.G, g = u % kv.G, H = p.H;
   const VisibleTiles<kUnit> vt(kv.length(r, nullptr), p.window, p.sinks);
   if (chunk > 0 && static_cast<int64_t>(chunk) * (kJoinTokens / kUnit) >= vt.count) return;
-  int64_t all = 0, before = 0;
-  for (int x = tid; x < kv.R; x += kJoinThreads) {
-    const int c = VisibleTiles<kUnit>(kv.length(x, nullptr), p.window, p.sinks).count;
-    all += c;
-    if (x < r) before += c;
-  }
-  int64_t U, base;
-  block_scan<kJoinThreads>(all, scan_part[0], U);
-  block_scan<kJoinThreads>(before, scan_part[1], base);
-  U *= kv.G;
-  base = base * kv.G + static_cast<int64_t>(g) * vt.count;
-  int b0 = 0, b1 = 0;
-  if (vt.count) {
-    const int nb = sharing(U, p.blocks);
-    b0 = block_of_unit(U, base, nb);
-    b1 = block_of_unit(U, base + vt.count - 1, nb);
-  }
+  int b0, b1;
+  blocks_of_row<kJoinThreads>(p, r, g, vt, scan_part, b0, b1);
   pdl_wait();
   if (vt.count == 0) {
-    for (int e = tid; e < H * kD; e += kJoinThreads) p.out[static_cast<size_t>(u) * H * kD + e] = 0.f;
-    if (p.lse && tid < H) p.lse[static_cast<size_t>(u) * H + tid] = ninf;
+    write_nothing(p, u);
     return;
   }
   if (b0 == b1) {
     if (!kWeights) return;
     if (tid < H) s_lse2[tid] = p.lse2[static_cast<size_t>(u) * H + tid];
   } else {
-    // part x: block b0 + x, in its second slot where the row begins. A head's
-    // parts are dealt to `ways` warps, each of which finds their maximum and
+    // a head's parts are dealt to `ways` warps, each of which finds their maximum and
     // sum for itself and adds up its own outputs.
     const int parts = b1 - b0 + 1;
     const int shift = H <= 1 ? 0 : (H <= 2 ? 1 : (H <= 4 ? 2 : 3)), heads = 1 << shift, ways = kJoinWarps >> shift;
     const int h = warp & (heads - 1), way = warp >> shift;
     if (h < H) {
-      const int64_t slot = static_cast<int64_t>(H) * kPartRow;
-      const float* const first = p.part + (static_cast<int64_t>(b0) * kPartSlots + 1) * slot + h * kPartRow;
-      const float* const rest = first - slot;
-      auto part = [&](int x) { return x == 0 ? first : rest + x * kPartSlots * slot; };
+      const Parts part(p, b0, h);
       float M = ninf, L = 0.f;  // of the parts lane, lane + 32, ...
       for (int x = lane; x < parts; x += 32) {
         const float2 v = *reinterpret_cast<const float2*>(part(x));
@@ -672,8 +790,11 @@ kvs_status launch(const DecodeParams& p, const CUtensorMap& mk, const CUtensorMa
   allow_smem<paged_decode_kernel<kF32Q, kWeights>>(sizeof(DecodeSmem));
   launch_chained(paged_decode_kernel<kF32Q, kWeights>, dim3(p.blocks), dim3(kThreads), sizeof(DecodeSmem), s, p, mk,
                  mv);
-  launch_chained(paged_decode_join_kernel<kWeights>, dim3(static_cast<unsigned>(joins)), dim3(kJoinThreads), 0, s, p,
-                 static_cast<int>(chunks));
+  if (!kWeights && joins <= sm_count())
+    launch_chained(paged_decode_join_few_kernel, dim3(static_cast<unsigned>(joins)), dim3(kJoinThreads), 0, s, p);
+  else
+    launch_chained(paged_decode_join_kernel<kWeights>, dim3(static_cast<unsigned>(joins)), dim3(kJoinThreads), 0, s, p,
+                   static_cast<int>(chunks));
   return check_launch("paged_decode_attn");
 }
 

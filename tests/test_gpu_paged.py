@@ -186,6 +186,19 @@ def test_decode_splits_head_counts(kvs, H, weights, qdt):
     ref.check_decode(out, lse, q, k, v, table, lens, 0, 0, SC, torch.zeros_like(mass) if weights else None, mass)
 
 
+@pytest.mark.parametrize("H", [1, 3, 4, 8])
+@pytest.mark.parametrize("weights", [False, True])
+def test_decode_one_long_row_among_many(kvs, H, weights):
+    """More rows than SMs, one of them cut into many parts."""
+    lens = [0, 50, 25003] + [17 * i % 90 for i in range(200)]
+    k, v, table, n = ref.make(lens, 1, 64, seed=H, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(len(lens), 1, H, D, device=DEV)
+    mass = torch.zeros(len(lens), 1, cache.cap, device=DEV) if weights else None
+    out, lse = kvs.paged_decode_attn(q, cache, mass=mass)
+    ref.check_decode(out, lse, q, k, v, table, lens, 0, 0, SC, torch.zeros_like(mass) if weights else None, mass)
+
+
 def test_decode_extreme_logits(kvs):
     """Logits from -3e4 to 3e4 and equal ones: the running maximum carries every one."""
     lens = [700, 700]
