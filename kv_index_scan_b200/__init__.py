@@ -11,7 +11,6 @@ the library has not been built.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -559,18 +558,19 @@ def decode_step(q, index: FathomIndex, n, B: int, k: int, fullK, fullV, slot_map
 
 # ----------------------------------------------------------------------------- the paged K/V cache
 
-_SAME_DEVICE = contextlib.nullcontext()
+def _elsewhere(dev: torch.device, stream) -> bool:
+    """Whether a call has to go into a context first: its tensors' device is not the current one, or it has a
+    stream of its own."""
+    return stream is not None or torch.cuda.current_device() != dev.index
 
 
 def _on(dev: torch.device, stream):
-    """The context a call runs in: its tensors' device current and, where one is given, `stream`
-    current too, so that what the call allocates belongs to the stream that uses it."""
-    if stream is not None:
-        _require(stream.device == dev, f"the stream is on {stream.device}, the cache on {dev}")
-        return torch.cuda.stream(stream)
-    if torch.cuda.current_device() == dev.index:
-        return _SAME_DEVICE
-    return torch.cuda.device(dev)
+    """That context: dev current and, where one is given, `stream` current too, so that what the call
+    allocates belongs to the stream that uses it."""
+    if stream is None:
+        return torch.cuda.device(dev)
+    _require(stream.device == dev, f"the stream is on {stream.device}, the cache on {dev}")
+    return torch.cuda.stream(stream)
 
 
 def _raw_stream(dev: torch.device) -> int:
@@ -649,6 +649,9 @@ def paged_append(cache: PagedKV, Knew: torch.Tensor, Vnew: torch.Tensor, cu=None
     packed by request with cu int32 [R+1] (None: one token each). cache.n already counts them. mass f32 and
     pos int32 [R][G][cap] get 0 and the token's place (counted by seen int32 [R])."""
     dev = cache.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return paged_append(cache, Knew, Vnew, cu, mass, pos, seen, None, dev_status)
     shape = Knew.shape
     if not (len(shape) == 3 and Vnew.shape == shape and shape[1] == cache.G and shape[2] == cache.D
             and Knew.dtype is torch.bfloat16 and Vnew.dtype is torch.bfloat16 and Knew.device == dev
@@ -662,17 +665,17 @@ def paged_append(cache: PagedKV, Knew: torch.Tensor, Vnew: torch.Tensor, cu=None
     cup = None if cu is None else _need("cu", cu, cache._cu_shape, torch.int32, dev).data_ptr()
     sp = None if seen is None else _need("seen", seen, cache._r_shape, torch.int32, dev).data_ptr()
     mp, pp = cache._state("mass", mass, torch.float32), cache._state("pos", pos, torch.int32)
-    with _on(dev, stream):
-        _check(_lib.kvs_paged_append(cache._ref, Knew.data_ptr(), Vnew.data_ptr(), ld, cup, T, mp, pp, sp,
-                                     _ptr(dev_status), _raw_stream(dev)),
-               "kvs_paged_append")
+    _check(_lib.kvs_paged_append(cache._ref, Knew.data_ptr(), Vnew.data_ptr(), ld, cup, T, mp, pp, sp,
+                                 _ptr(dev_status), _raw_stream(dev)), "kvs_paged_append")
 
 
 def paged_decode_workspace(cache: PagedKV, H: int, weights: bool = False) -> torch.Tensor:
     """A workspace for paged_decode_attn, for callers that keep one (calls that may run at the same time
     need one each)."""
-    with _on(cache.device, None):
-        return cache._workspace("kvs_paged_decode_workspace_size", H, cache.cap if weights else 0)
+    if _elsewhere(cache.device, None):
+        with _on(cache.device, None):
+            return paged_decode_workspace(cache, H, weights)
+    return cache._workspace("kvs_paged_decode_workspace_size", H, cache.cap if weights else 0)
 
 
 def paged_decode_attn(q: torch.Tensor, cache: PagedKV, window: int = 0, sinks: int = 0, scale: float | None = None,
@@ -681,33 +684,35 @@ def paged_decode_attn(q: torch.Tensor, cache: PagedKV, window: int = 0, sinks: i
     [R][G][H][128], lse f32 [R][G][H]). window > 0: only the last `window` tokens and the first `sinks`.
     mass f32 [R][G][cap]: every visible token's softmax weights, summed over the H heads, are added to it
     (in place, or into mass_out)."""
-    dev, R, G = cache.device, cache.R, cache.G
+    dev, R, G, D = cache.device, cache.R, cache.G, cache.D
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return paged_decode_attn(q, cache, window, sinks, scale, out, lse, mass, mass_out, ws, None, dev_status)
     _counts(window=window, sinks=sinks)
-    H = q.shape[2] if q.dim() == 4 else 0
-    qd = q.dtype
-    if qd != torch.bfloat16:
-        qd = torch.float32
-    _need("q", q, (R, G, H, cache.D), qd, dev)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty(R, G, H, cache.D, dtype=torch.float32, device=dev)
-        else:
-            _need("out", out, (R, G, H, cache.D), torch.float32, dev)
-        if lse is None:
-            lse = torch.empty(R, G, H, dtype=torch.float32, device=dev)
-        else:
-            _need("lse", lse, (R, G, H), torch.float32, dev)
-        mp = cache._state("mass", mass, torch.float32)
-        mo = mp if mass_out is None else cache._state("mass_out", mass_out, torch.float32)
-        if ws is None:
-            ws = paged_decode_workspace(cache, H, mass is not None)
-        else:
-            _check_ws(ws, dev)
-        a = PagedDecodeArgsC(cache._ref, q.data_ptr(), KVS_BF16 if qd == torch.bfloat16 else KVS_F32, H, window,
-                             sinks, 1.0 / math.sqrt(cache.D) if scale is None else scale, out.data_ptr(),
-                             lse.data_ptr(), mp, mo)
-        _check(_lib.paged_decode_attn(ctypes.byref(a), ws.data_ptr(), ws.numel(), _ptr(dev_status),
-                                      _raw_stream(dev)), "paged_decode_attn")
+    shape, bf16 = q.shape, q.dtype is torch.bfloat16
+    if not (len(shape) == 4 and shape[0] == R and shape[1] == G and shape[3] == D
+            and (bf16 or q.dtype is torch.float32) and q.device == dev and q.is_contiguous()):
+        raise ValueError(f"q must be contiguous f32 or bf16 [{R}][{G}][H][{D}] on {dev}, got {q.dtype} {tuple(shape)} "
+                         f"on {q.device}")
+    H = shape[2]
+    if out is None:
+        out = torch.empty(R, G, H, D, dtype=torch.float32, device=dev)
+    else:
+        _need("out", out, shape, torch.float32, dev)
+    if lse is None:
+        lse = torch.empty(R, G, H, dtype=torch.float32, device=dev)
+    else:
+        _need("lse", lse, shape[:3], torch.float32, dev)
+    mp = cache._state("mass", mass, torch.float32)
+    mo = mp if mass_out is None else cache._state("mass_out", mass_out, torch.float32)
+    if ws is None:
+        ws = paged_decode_workspace(cache, H, mass is not None)
+    else:
+        _check_ws(ws, dev)
+    a = PagedDecodeArgsC(cache._ref, q.data_ptr(), KVS_BF16 if bf16 else KVS_F32, H, window, sinks,
+                         1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), lse.data_ptr(), mp, mo)
+    _check(_lib.paged_decode_attn(ctypes.byref(a), ws.data_ptr(), ws.numel(), _ptr(dev_status), _raw_stream(dev)),
+           "paged_decode_attn")
     return out, lse
 
 
@@ -718,6 +723,9 @@ def paged_prompt_attn(q: torch.Tensor, cu: torch.Tensor, cache: PagedKV, window:
     itself and the window - 1 before it, and the first `sinks`. Rows from cu[R] on are left as they are
     (zero in an `out` and `lse` made here)."""
     dev = cache.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return paged_prompt_attn(q, cu, cache, window, sinks, scale, out, lse, None, dev_status)
     _counts(window=window, sinks=sinks)
     shape = q.shape
     if not (len(shape) == 3 and q.dtype is torch.bfloat16 and q.device == dev and shape[2] == cache.D
@@ -725,24 +733,23 @@ def paged_prompt_attn(q: torch.Tensor, cu: torch.Tensor, cache: PagedKV, window:
         raise ValueError(f"q must be bf16 [T][{cache.G}*H][{cache.D}] on {dev}")
     T, Hq, D = shape
     _need("cu", cu, cache._cu_shape, torch.int32, dev)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device=dev)
-        else:
-            if not (out.shape == shape and out.dtype is torch.bfloat16 and out.device == dev):
-                raise ValueError(f"out must be bf16 {tuple(shape)} on {dev}")
-        qs, os_ = q.stride(), out.stride()
-        if not (qs[2] == 1 and os_[2] == 1 and (Hq == 1 or (qs[1] == D and os_[1] == D))):
-            raise ValueError("q and out must have contiguous heads")
-        if lse is None:
-            lse = torch.zeros(T, Hq, dtype=torch.float32, device=dev)
-        else:
-            _need("lse", lse, (T, Hq), torch.float32, dev)
-        ld = (qs[0], os_[0]) if T > 1 else (Hq * D, Hq * D)
-        a = PagedPromptArgsC(cache._ref, q.data_ptr(), ld[0], cu.data_ptr(), T, Hq // cache.G, window, sinks,
-                             1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), ld[1], lse.data_ptr())
-        _check(_lib.paged_prompt_attn(ctypes.byref(a), _ptr(dev_status), _raw_stream(dev)),
-               "paged_prompt_attn")
+    if out is None:
+        out = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    else:
+        if not (out.shape == shape and out.dtype is torch.bfloat16 and out.device == dev):
+            raise ValueError(f"out must be bf16 {tuple(shape)} on {dev}")
+    qs, os_ = q.stride(), out.stride()
+    if not (qs[2] == 1 and os_[2] == 1 and (Hq == 1 or (qs[1] == D and os_[1] == D))):
+        raise ValueError("q and out must have contiguous heads")
+    if lse is None:
+        lse = torch.zeros(T, Hq, dtype=torch.float32, device=dev)
+    else:
+        _need("lse", lse, (T, Hq), torch.float32, dev)
+    ld = (qs[0], os_[0]) if T > 1 else (Hq * D, Hq * D)
+    a = PagedPromptArgsC(cache._ref, q.data_ptr(), ld[0], cu.data_ptr(), T, Hq // cache.G, window, sinks,
+                         1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), ld[1], lse.data_ptr())
+    _check(_lib.paged_prompt_attn(ctypes.byref(a), _ptr(dev_status), _raw_stream(dev)),
+           "paged_prompt_attn")
     return out, lse
 
 
@@ -756,26 +763,29 @@ def paged_evict(cache: PagedKV, mass: torch.Tensor, budget: int, sinks: int = 0,
     place unless mass_out, pos_out and n_out are given. -> src int32 [R][G][budget]: the slot each token was
     in (-1 behind the last)."""
     dev = cache.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return paged_evict(cache, mass, budget, sinks, recent, pos, seen, mass_out, pos_out, n_out, src, ws, None,
+                               dev_status)
     _counts(budget=budget, sinks=sinks, recent=recent)
-    with _on(dev, stream):
-        mp = cache._state("mass", mass, torch.float32)
-        _require(mp is not None, "mass is required")
-        mo = mp if mass_out is None else cache._state("mass_out", mass_out, torch.float32)
-        pp = cache._state("pos", pos, torch.int32)
-        _require(pp is not None or pos_out is None, "pos_out without pos")
-        po = pp if pos_out is None else cache._state("pos_out", pos_out, torch.int32)
-        sp = None if seen is None else _need("seen", seen, cache._r_shape, torch.int32, dev).data_ptr()
-        no = (cache.n if n_out is None else _need("n_out", n_out, cache._r_shape, torch.int32, dev)).data_ptr()
-        _require(budget >= 1, "budget must be at least 1")
-        if src is None:
-            src = torch.empty(cache.R, cache.G, budget, dtype=torch.int32, device=dev)
-        else:
-            _need("src", src, (cache.R, cache.G, budget), torch.int32, dev)
-        if ws is None:
-            ws = cache._workspace("kvs_paged_evict_workspace_size", budget)
-        else:
-            _check_ws(ws, dev)
-        a = PagedEvictArgsC(cache._ref, mp, pp, sp, budget, sinks, recent, mo, po, no, src.data_ptr())
-        _check(_lib.kvs_paged_evict(ctypes.byref(a), ws.data_ptr(), ws.numel(), _ptr(dev_status),
-                                    _raw_stream(dev)), "kvs_paged_evict")
+    mp = cache._state("mass", mass, torch.float32)
+    _require(mp is not None, "mass is required")
+    mo = mp if mass_out is None else cache._state("mass_out", mass_out, torch.float32)
+    pp = cache._state("pos", pos, torch.int32)
+    _require(pp is not None or pos_out is None, "pos_out without pos")
+    po = pp if pos_out is None else cache._state("pos_out", pos_out, torch.int32)
+    sp = None if seen is None else _need("seen", seen, cache._r_shape, torch.int32, dev).data_ptr()
+    no = (cache.n if n_out is None else _need("n_out", n_out, cache._r_shape, torch.int32, dev)).data_ptr()
+    _require(budget >= 1, "budget must be at least 1")
+    if src is None:
+        src = torch.empty(cache.R, cache.G, budget, dtype=torch.int32, device=dev)
+    else:
+        _need("src", src, (cache.R, cache.G, budget), torch.int32, dev)
+    if ws is None:
+        ws = cache._workspace("kvs_paged_evict_workspace_size", budget)
+    else:
+        _check_ws(ws, dev)
+    a = PagedEvictArgsC(cache._ref, mp, pp, sp, budget, sinks, recent, mo, po, no, src.data_ptr())
+    _check(_lib.kvs_paged_evict(ctypes.byref(a), ws.data_ptr(), ws.numel(), _ptr(dev_status),
+                                _raw_stream(dev)), "kvs_paged_evict")
     return src

@@ -156,8 +156,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
   extern __shared__ __align__(1024) unsigned char decode_smem[];
   DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>(decode_smem);
   __shared__ int64_t scan_part[kThreads / 32];
-  __shared__ int64_t s_base;
-  __shared__ int s_r;
+  __shared__ int s_r, s_n, s_g, s_k;  // where the run begins: request, its length, KV head, tile
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PagedView& kv = p.kv;
   const int G = kv.G;
@@ -178,8 +177,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
   const int per = (kv.R + kThreads - 1) / kThreads;
   const int r_lo = min(kv.R, tid * per), r_hi = min(kv.R, r_lo + per);
   int64_t mine = 0;
-  for (int r = r_lo; r < r_hi; ++r)
-    mine += VisibleTiles<kUnit>(kv.length(r, p.dev_status), p.window, p.sinks).count;
+  int n_lo = 0;
+  for (int r = r_lo; r < r_hi; ++r) {
+    const int n = kv.length(r, p.dev_status);
+    if (r == r_lo) n_lo = n;
+    mine += VisibleTiles<kUnit>(n, p.window, p.sinks).count;
+  }
   int64_t U;
   int64_t before = block_scan<kThreads>(mine, scan_part, U) * G;
   U *= G;
@@ -187,14 +190,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
   if (static_cast<int>(blockIdx.x) >= nb) return;
   const int64_t u0 = first_unit(U, blockIdx.x, nb), u1 = first_unit(U, blockIdx.x + 1, nb);
   if (u0 >= before && u0 < before + mine * G) {
-    int r = r_lo;
-    for (;; ++r) {
-      const int64_t c = static_cast<int64_t>(VisibleTiles<kUnit>(kv.length(r, nullptr), p.window, p.sinks).count) * G;
-      if (u0 < before + c) break;
-      before += c;
+    int r = r_lo, n = n_lo, count;
+    for (;; n = kv.length(++r, nullptr)) {
+      count = VisibleTiles<kUnit>(n, p.window, p.sinks).count;
+      if (u0 < before + static_cast<int64_t>(count) * G) break;
+      before += static_cast<int64_t>(count) * G;
     }
+    const int64_t into = u0 - before;
+    const int g = into >> 31 ? static_cast<int>(into / count) : static_cast<int>(into) / count;  // (64 bits are slow)
     s_r = r;
-    s_base = before;
+    s_n = n;
+    s_g = g;
+    s_k = static_cast<int>(into - static_cast<int64_t>(g) * count);
   }
   __syncthreads();
   const int units = static_cast<int>(u1 - u0);
@@ -210,9 +217,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
     const int rows = min(1 << kv.shift, kUnit), copies = 2 * (kUnit / rows);
     const bool isv = lane & 1;
     const int sub = lane >> 1;  // this lane's page within the unit
-    int r = s_r;
-    VisibleTiles<kUnit> vt(kv.length(r, nullptr), p.window, p.sinks);
-    int k = static_cast<int>((u0 - s_base) % vt.count), g = static_cast<int>((u0 - s_base) / vt.count);
+    int r = s_r, g = s_g, k = s_k;
+    VisibleTiles<kUnit> vt(s_n, p.window, p.sinks);
     const int k_start = k;
     UnitInfo next;
     int next_id;
@@ -302,6 +308,23 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
   float o[8][4];
   float mA = ninf, mB = ninf, lA = 0.f, lB = 0.f;
 
+  // a row's queries, head = fragment column gq
+  auto load_q = [&](int row) {
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const size_t at = (static_cast<size_t>(row) * H + min(gq, H - 1)) * kD + 16 * ks + 8 * e + 2 * tq;
+        if constexpr (kF32Q) {
+          float2 v = *reinterpret_cast<const float2*>(static_cast<const float*>(p.q) + at);
+#pragma unroll
+          for (int s = 0; s < 3; ++s) qf[s][ks][e] = take_bf16(v.x, v.y);
+        } else {
+          qf[0][ks][e] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) + at);
+        }
+      }
+  };
+  load_q(s_r * G + s_g);  // while the first unit is on its way
   for (int i = 0; i < units; ++i) {
     const int st = i % kStages;
     int ok = 1;
@@ -314,20 +337,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
     if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
     const UnitInfo info = sm.info[st];
     if (info.flags & kFirst) {
-      // a new row: its queries, head = fragment column gq
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const size_t at = (static_cast<size_t>(info.row) * H + min(gq, H - 1)) * kD + 16 * ks + 8 * e + 2 * tq;
-          if constexpr (kF32Q) {
-            float2 v = *reinterpret_cast<const float2*>(static_cast<const float*>(p.q) + at);
-#pragma unroll
-            for (int s = 0; s < 3; ++s) qf[s][ks][e] = take_bf16(v.x, v.y);
-          } else {
-            qf[0][ks][e] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) + at);
-          }
-        }
+      // a new row
+      if (i > 0) load_q(info.row);
 #pragma unroll
       for (int d = 0; d < 8; ++d)
 #pragma unroll
