@@ -128,8 +128,10 @@ def _declare():
     L.paged_decode_attn.restype = I32
     L.kvs_paged_decode_workspace_size.argtypes = [I32, I32, I32, I32]
     L.kvs_paged_decode_workspace_size.restype = SZ
-    L.paged_prompt_attn.argtypes = [ctypes.POINTER(PagedPromptArgsC), P, P]
+    L.paged_prompt_attn.argtypes = [ctypes.POINTER(PagedPromptArgsC), P, SZ, P, P]
     L.paged_prompt_attn.restype = I32
+    L.kvs_paged_prompt_workspace_size.argtypes = [I32, I32, I32, I32, I32]
+    L.kvs_paged_prompt_workspace_size.restype = SZ
     L.kvs_paged_evict.argtypes = [ctypes.POINTER(PagedEvictArgsC), P, SZ, P, P]
     L.kvs_paged_evict.restype = I32
     L.kvs_paged_evict_workspace_size.argtypes = [I32, I32, I32]
@@ -636,11 +638,14 @@ class PagedKV:
     def _state(self, name, t, dtype):
         return None if t is None else _need(name, t, self._state_shape, dtype, self.device).data_ptr()
 
-    def _workspace(self, query, *sizes) -> torch.Tensor:
+    def _workspace(self, query, *sizes):
+        """What the library asks for, or None where that is nothing."""
         nb = self._ws_bytes.get((query, sizes))
         if nb is None:
-            nb = self._ws_bytes[query, sizes] = max(int(getattr(_lib, query)(self.R, self.G, *sizes)), 16)
-        return torch.empty(nb, dtype=torch.uint8, device=self.device)
+            if len(self._ws_bytes) > 1000:  # a prompt's size depends on its tokens
+                self._ws_bytes.clear()
+            nb = self._ws_bytes[query, sizes] = int(getattr(_lib, query)(self.R, self.G, *sizes))
+        return torch.empty(nb, dtype=torch.uint8, device=self.device) if nb else None
 
 
 def paged_append(cache: PagedKV, Knew: torch.Tensor, Vnew: torch.Tensor, cu=None, mass=None, pos=None, seen=None,
@@ -717,7 +722,7 @@ def paged_decode_attn(q: torch.Tensor, cache: PagedKV, window: int = 0, sinks: i
 
 
 def paged_prompt_attn(q: torch.Tensor, cu: torch.Tensor, cache: PagedKV, window: int = 0, sinks: int = 0,
-                      scale: float | None = None, out=None, lse=None, stream=None, dev_status=None):
+                      scale: float | None = None, out=None, lse=None, ws=None, stream=None, dev_status=None):
     """Causal attention of the newest tokens of each request over its cache: q bf16 [T][G*H][128], packed by
     request with cu int32 [R+1] -> (out bf16 [T][G*H][128], lse f32 [T][G*H]). window > 0: each token sees
     itself and the window - 1 before it, and the first `sinks`. Rows from cu[R] on are left as they are
@@ -725,7 +730,7 @@ def paged_prompt_attn(q: torch.Tensor, cu: torch.Tensor, cache: PagedKV, window:
     dev = cache.device
     if _elsewhere(dev, stream):
         with _on(dev, stream):
-            return paged_prompt_attn(q, cu, cache, window, sinks, scale, out, lse, None, dev_status)
+            return paged_prompt_attn(q, cu, cache, window, sinks, scale, out, lse, ws, None, dev_status)
     _counts(window=window, sinks=sinks)
     shape = q.shape
     if not (len(shape) == 3 and q.dtype is torch.bfloat16 and q.device == dev and shape[2] == cache.D
@@ -748,8 +753,15 @@ def paged_prompt_attn(q: torch.Tensor, cu: torch.Tensor, cache: PagedKV, window:
     ld = (qs[0], os_[0]) if T > 1 else (Hq * D, Hq * D)
     a = PagedPromptArgsC(cache._ref, q.data_ptr(), ld[0], cu.data_ptr(), T, Hq // cache.G, window, sinks,
                          1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), ld[1], lse.data_ptr())
-    _check(_lib.paged_prompt_attn(ctypes.byref(a), _ptr(dev_status), _raw_stream(dev)),
-           "paged_prompt_attn")
+    if ws is None:
+        ws = cache._workspace("kvs_paged_prompt_workspace_size", Hq // cache.G, T, cache.cap)
+    else:
+        _check_ws(ws, dev)
+    if ws is None:
+        wp = wn = 0
+    else:
+        wp, wn = ws.data_ptr(), ws.numel()
+    _check(_lib.paged_prompt_attn(ctypes.byref(a), wp, wn, _ptr(dev_status), _raw_stream(dev)), "paged_prompt_attn")
     return out, lse
 
 

@@ -107,7 +107,12 @@ kvs_status paged_decode_attn(const kvs_paged_decode_args* a, void* ws, size_t ws
   return ok();
 }
 
-kvs_status paged_prompt_attn(const kvs_paged_prompt_args* a, int32_t* dev_status, void* stream) {
+size_t kvs_paged_prompt_workspace_size(int32_t R, int32_t G, int32_t H, int32_t T, int32_t cap) {
+  return paged_prompt_ws_bytes(R, G, H, T, cap);
+}
+
+kvs_status paged_prompt_attn(const kvs_paged_prompt_args* a, void* ws, size_t ws_bytes, int32_t* dev_status,
+                             void* stream) {
   KVS_REQUIRE(a != nullptr, KVS_EINVAL, "paged_prompt_attn: args is null");
   KVS_PROPAGATE(check_paged("paged_prompt_attn", a->kv));
   KVS_PROPAGATE(check_mask("paged_prompt_attn", a->window, a->sinks, a->scale));
@@ -122,7 +127,11 @@ kvs_status paged_prompt_attn(const kvs_paged_prompt_args* a, int32_t* dev_status
   KVS_REQUIRE(static_cast<int64_t>(a->T) * a->H < (1ll << 31) - 4096, KVS_EUNSUPPORTED,
               "paged_prompt_attn: T*H=%lld rows (below 2^31)", static_cast<long long>(a->T) * a->H);
   KVS_REQUIRE(aligned16(a->q) && aligned16(a->out), KVS_EINVAL, "paged_prompt_attn: q and out must be 16-byte aligned");
-  KVS_PROPAGATE(paged_prompt_launch(a, dev_status, static_cast<cudaStream_t>(stream)));
+  const size_t need = paged_prompt_ws_bytes(a->kv->R, a->kv->G, a->H, a->T, a->kv->max_pages * a->kv->page);
+  KVS_REQUIRE(need == 0 || (ws && ws_bytes >= need), KVS_EWORKSPACE, "paged_prompt_attn: workspace %zu < %zu bytes",
+              ws_bytes, need);
+  KVS_REQUIRE(aligned16(ws), KVS_EINVAL, "paged_prompt_attn: the workspace must be 16-byte aligned");
+  KVS_PROPAGATE(paged_prompt_launch(a, ws, dev_status, static_cast<cudaStream_t>(stream)));
   return ok();
 }
 

@@ -13,7 +13,9 @@
 //    share a KV head share its K and V. It walks the 128-token tiles that any of
 //    its rows sees, the sinks' first. Blocks are persistent, one an SM, each
 //    with an equal share of the items; the next item's loads and first products
-//    begin while the last one's rows are written.
+//    begin while the last one's rows are written. Where there are fewer items
+//    than SMs (a few tokens over a long cache), an item's tiles are split in
+//    pieces that are items themselves, and a second kernel joins the parts.
 //  * One warp brings Q (a copy per row tile and 128-byte half), and K and V (a
 //    copy per page and half, into two stages each) by TMA in the operand layout
 //    of the tensor cores (128-byte swizzle). K is read K-major; V as it lies,
@@ -39,6 +41,8 @@
 // winds down with no copy in flight and its tensor memory freed.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "async.cuh"
 
 namespace kvs {
@@ -55,6 +59,8 @@ constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kCle
 constexpr int kThreads = 32 * 12;             // three warpgroups
 // registers a thread: 168 at launch; 8 * 208 + 4 * 88 = 12 * 168
 constexpr int kSoftRegs = 208, kOtherRegs = 88;
+constexpr int kMaxPieces = 32;               // of an item (a lane of the join each)
+constexpr int kPieceTiles = 8;               // of the longest request, at least (1024 tokens: 20.6 us whole, 23.1 in two)
 constexpr float kGrow = 8.f;                 // log2 of the growth that a maximum may lag behind
 
 struct PromptSmem {
@@ -78,6 +84,9 @@ struct PromptParams {
   uint16_t* out;
   int64_t out_ld;
   float* lse;
+  int pieces;        // of an item's tiles, each an item of its own (1: not split)
+  float* part_o;     // [pieces][T][G*H][128], relative to the row's maximum in that piece
+  float2* part_ml;   // [pieces][T][G*H]: that maximum (base 2), the sum
   int32_t* dev_status;
 
   // the first packed row of request r, within the T there are
@@ -206,28 +215,39 @@ __device__ __forceinline__ uint32_t low_bits(int x) { return x <= 0 ? 0u : (x >=
 // The rows of `per` tokens of a request and KV head for each of two row tiles,
 // and the tiles of 128 tokens that any of them sees: the sinks', then those from
 // the first row's window to the last row's own token.
+template <bool kPieces>
 struct Item {
   int r, g, q0;          // request, KV head, first packed row of the request
   int tok0, c;           // first token of the item among the request's c new ones
   int p_lo;              // its position
   int end, lo;           // tokens seen at most; first token of the first row's window
-  int nsink, first, tiles;
+  int nsink, first;      // leading tiles with sinks; tile of the window's first token
+  int piece, from, tiles;  // the item's tiles from, from + 1, ... of all
 
-  __device__ __forceinline__ int token(int i) const { return (i < nsink ? i : first + i - nsink) * kTok; }
+  __device__ __forceinline__ int token(int i) const {
+    const int x = kPieces ? from + i : i;
+    return (x < nsink ? x : first + x - nsink) * kTok;
+  }
   // whether a row of the tile at t0 is seen by no row, or was not loaded
   __device__ __forceinline__ bool ragged(int t0, int there, int sinks) const {
     return there != 0xFF || t0 + kTok > end || (t0 < lo && t0 + kTok > sinks);
   }
 };
 
-// Item x of all, found by the whole warp: KV heads innermost, the blocks of a
-// request from its last (which sees most) to its first, the last request first.
+// Item x of all, found by the whole warp: its pieces innermost, then the KV heads,
+// the blocks of a request from its last (which sees most) to its first, the last request first.
 // False behind the last one.
-__device__ __forceinline__ bool find_item(const PromptParams& p, uint32_t x, Item& it) {
+template <bool kPieces>
+__device__ __forceinline__ bool find_item(const PromptParams& p, uint32_t x, Item<kPieces>& it) {
   const PagedView& kv = p.kv;
   const int lane = threadIdx.x & 31;
-  const uint32_t order = x / static_cast<uint32_t>(kv.G);
-  it.g = static_cast<int>(x - order * kv.G);
+  uint32_t whole = x;
+  if constexpr (kPieces) {
+    whole = x / static_cast<uint32_t>(p.pieces);
+    it.piece = static_cast<int>(x - whole * p.pieces);
+  }
+  const uint32_t order = whole / static_cast<uint32_t>(kv.G);
+  it.g = static_cast<int>(whole - order * kv.G);
   uint32_t base = 0;
   for (int top = kv.R; top > 0; top -= 32) {
     const int r = top - 1 - lane;
@@ -266,6 +286,11 @@ __device__ __forceinline__ bool find_item(const PromptParams& p, uint32_t x, Ite
         }
       }
       it.tiles = it.nsink + (it.end + kTok - 1) / kTok - it.first;
+      if constexpr (kPieces) {
+        const int64_t tiles = it.tiles;
+        it.from = static_cast<int>(tiles * it.piece / p.pieces);
+        it.tiles = static_cast<int>(tiles * (it.piece + 1) / p.pieces) - it.from;
+      }
       return true;
     }
     base += __shfl_sync(0xFFFFFFFFu, inc, 31);
@@ -273,6 +298,7 @@ __device__ __forceinline__ bool find_item(const PromptParams& p, uint32_t x, Ite
   return false;
 }
 
+template <bool kPieces>
 __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptParams p,
                                                                    const __grid_constant__ CUtensorMap mapQ,
                                                                    const __grid_constant__ CUtensorMap mapK,
@@ -286,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
   // blocks and in the reverse in turn (items shrink along the order). Every warp
   // finds them for itself.
   uint32_t round = 0;
-  auto next_item = [&](Item& it) {
+  auto next_item = [&](Item<kPieces>& it) {
     const uint32_t at = round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
     return find_item(p, round++ * gridDim.x + at, it);
   };
@@ -321,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
   }
   pdl_wait();
   pdl_trigger();
-  Item it;
+  Item<kPieces> it;
   bool more = next_item(it);
   fence_before();
   __syncthreads();
@@ -625,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
         l += z0 + z1;
       }
       // the next item is found while this one's last products run
-      const Item was = it;
+      const Item<kPieces> was = it;
       more = next_item(it);
       // ---------------- the rows' output ----------------
       bool done = ok && was.tiles > 0;
@@ -640,6 +666,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
       auto there = [&](int x) { return x < p.per * H && tok + token_of(x) < was.c; };
       auto token_row = [&](int x) { return static_cast<int64_t>(was.q0 + tok + token_of(x)); };
       auto head_of = [&](int x) { return was.g * H + x - token_of(x) * H; };
+      if constexpr (kPieces) {
+        // a part: the row as it is, for the join
+        const int64_t row = there(tid & 127)
+                                ? (was.piece * static_cast<int64_t>(p.T) + token_row(tid & 127)) * G * H + head_of(tid & 127)
+                                : -1;
+        if (row >= 0) p.part_ml[row] = done ? make_float2(m, l) : make_float2(ninf, 0.f);
+#pragma unroll 1
+        for (int e = 0; e < 4 && done; ++e) {
+          float o[32];
+          tmem_ld32(o_at + 32 * e, o);
+          wait_ld();
+          if (row >= 0) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4*>(p.part_o + row * kD + 32 * e + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          }
+          __syncwarp();
+        }
+        fence_before();
+        continue;
+      }
       if (p.lse && there(tid & 127))
         p.lse[token_row(tid & 127) * G * H + head_of(tid & 127)] =
             l == 0.f ? ninf : (m + log2f(l)) * 0.6931471805599453f;
@@ -686,9 +733,82 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
   }
 }
 
+// The pieces of every (token, query head) row joined, a row a warp.
+__global__ void __launch_bounds__(256) paged_prompt_join_kernel(const PromptParams p) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t heads = static_cast<int64_t>(p.kv.G) * p.H, rows = heads * p.T;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row < p.start(0) * heads || row >= p.start(p.kv.R) * heads) return;
+  const float ninf = -__int_as_float(0x7f800000);
+  const float2 ml = lane < p.pieces ? p.part_ml[lane * rows + row] : make_float2(ninf, 0.f);
+  float M = ml.x;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+  // (a piece without a token of the row's has written nothing but this)
+  const bool none = ml.x == ninf && ml.y == 0.f;
+  const float c = none ? 0.f : exp2f(ml.x - (M == ninf ? 0.f : M));
+  float L = none ? 0.f : (ml.x == ninf ? ml.y : c * ml.y);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, d);
+  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+  const unsigned there = __ballot_sync(0xFFFFFFFFu, !none);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int x = 0; x < p.pieces; ++x) {
+    const float w = __shfl_sync(0xFFFFFFFFu, c, x) * inv;
+    if (!(there >> x & 1)) continue;
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (x * rows + row) * kD + 4 * lane);
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  }
+  const int64_t token = row / heads;
+  *reinterpret_cast<uint2*>(p.out + token * p.out_ld + (row - token * heads) * kD + 4 * lane) =
+      make_uint2(bf16_pair(o.x, o.y), bf16_pair(o.z, o.w));
+  if (p.lse && lane == 0) p.lse[row] = L == 0.f ? ninf : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// No more items than this, whatever the lengths: a part item a request, and whole ones.
+int64_t most_items(int R, int G, int H, int T) {
+  const int per2 = 2 * (kRows / H);
+  return (T / per2 + static_cast<int64_t>(T < R ? T : R)) * G;
+}
+
+// Pieces that an item's tiles are split in: as many as give every SM one where
+// the items do not, of at least kPieceTiles tiles of the longest request.
+int pieces_of(int R, int G, int H, int T, int64_t cap) {
+  const int64_t items = most_items(R, G, H, T);
+  if (items <= 0) return 1;
+  int64_t n = sm_count() / items;
+  if (n > kMaxPieces) n = kMaxPieces;
+  const int64_t most = (cap + kTok - 1) / kTok / kPieceTiles;
+  if (n > most) n = most;
+  return n < 1 ? 1 : static_cast<int>(n);
+}
+
+size_t carve(PromptParams* p, void* ws, int G, int H, int T, int pieces) {
+  if (pieces == 1) return 0;
+  WsCarver c(ws);
+  const size_t rows = static_cast<size_t>(pieces) * T * G * H;
+  float* o = c.take<float>(rows * kD);
+  float2* ml = c.take<float2>(rows);
+  if (p) {
+    p->part_o = o;
+    p->part_ml = ml;
+  }
+  return align_up(c.used, 16);
+}
+
 }  // namespace
 
-kvs_status paged_prompt_launch(const kvs_paged_prompt_args* a, int32_t* dev_status, cudaStream_t s) {
+size_t paged_prompt_ws_bytes(int R, int G, int H, int T, int cap) {
+  if (R < 1 || G < 1 || H < 1 || H > 8 || T < 1) return 0;
+  return carve(nullptr, nullptr, G, H, T, pieces_of(R, G, H, T, cap));
+}
+
+kvs_status paged_prompt_launch(const kvs_paged_prompt_args* a, void* ws, int32_t* dev_status, cudaStream_t s) {
   PromptParams p{};
   p.kv = paged_view(a->kv);
   p.cu = a->cu;
@@ -708,23 +828,32 @@ kvs_status paged_prompt_launch(const kvs_paged_prompt_args* a, int32_t* dev_stat
   KVS_PROPAGATE(paged_tensor_map(&mk, a->kv->K, p.kv, box, 1, "paged_prompt_attn"));
   KVS_PROPAGATE(paged_tensor_map(&mv, a->kv->V, p.kv, box, 1, "paged_prompt_attn"));
   KVS_PROPAGATE(query_tensor_map(&mq, a, p.per));
-  // no more items than this, whatever the lengths: a part item a request, and whole ones
-  const int64_t whole = a->T / (2 * p.per), part = a->T < p.kv.R ? a->T : p.kv.R;
-  const int64_t items = (whole + part) * p.kv.G;
+  p.pieces = pieces_of(p.kv.R, p.kv.G, p.H, p.T, static_cast<int64_t>(a->kv->max_pages) * a->kv->page);
+  carve(&p, ws, p.kv.G, p.H, p.T, p.pieces);
+  const int64_t items = most_items(p.kv.R, p.kv.G, p.H, p.T) * p.pieces;
   KVS_REQUIRE(items < (1ll << 31) - (1 << 20), KVS_EUNSUPPORTED, "paged_prompt_attn: T=%d queries of G=%d KV heads", a->T,
               p.kv.G);
-  // the register split must fit what the kernel is launched with, or the softmax
-  // warps would wait for registers that never come
-  static const int regs = [] {
-    cudaFuncAttributes f{};
-    return cudaFuncGetAttributes(&f, paged_prompt_kernel) == cudaSuccess ? f.numRegs : 0;
-  }();
-  KVS_REQUIRE(regs * kThreads >= 32 * kSoftWarps * kSoftRegs + (kThreads - 32 * kSoftWarps) * kOtherRegs, KVS_ECUDA,
-              "paged_prompt_attn: built with %d registers a thread", regs);
-  const int sms = sm_count();
-  allow_smem<paged_prompt_kernel>(sizeof(PromptSmem));
-  launch_chained(paged_prompt_kernel, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kThreads),
-                 sizeof(PromptSmem), s, p, mq, mk, mv);
+  const auto go = [&](auto kernel) -> kvs_status {
+    // the register split must fit what the kernel is launched with, or the softmax
+    // warps would wait for registers that never come
+    static const int regs = [&] {
+      cudaFuncAttributes f{};
+      return cudaFuncGetAttributes(&f, kernel.value) == cudaSuccess ? f.numRegs : 0;
+    }();
+    KVS_REQUIRE(regs * kThreads >= 32 * kSoftWarps * kSoftRegs + (kThreads - 32 * kSoftWarps) * kOtherRegs, KVS_ECUDA,
+                "paged_prompt_attn: built with %d registers a thread", regs);
+    const int sms = sm_count();
+    allow_smem<kernel.value>(sizeof(PromptSmem));
+    launch_chained(kernel.value, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kThreads),
+                   sizeof(PromptSmem), s, p, mq, mk, mv);
+    return KVS_OK;
+  };
+  KVS_PROPAGATE(p.pieces > 1 ? go(std::integral_constant<decltype(&paged_prompt_kernel<true>), paged_prompt_kernel<true>>())
+                             : go(std::integral_constant<decltype(&paged_prompt_kernel<false>), paged_prompt_kernel<false>>()));
+  if (p.pieces > 1) {
+    const int64_t rows = static_cast<int64_t>(p.T) * p.kv.G * p.H;
+    launch_chained(paged_prompt_join_kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, p);
+  }
   return check_launch("paged_prompt_attn");
 }
 

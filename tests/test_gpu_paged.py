@@ -376,6 +376,29 @@ def test_prompt_several_items_a_block(kvs, G, H, window, sinks):
     _prompt(kvs, [1500, 1700, 3, 700], [1500, 900, 3, 640], G, H, 32, window, sinks, seed=G)
 
 
+@pytest.mark.parametrize("H", [1, 4, 5, 8])
+@pytest.mark.parametrize("lens,new,G,page,window,sinks", [
+    ([9000], [3], 1, 64, 0, 0), ([9000, 100, 0, 5000], [5, 100, 0, 1], 2, 16, 0, 0),
+    ([20011, 700], [40, 2], 1, 128, 3000, 200), ([6000, 8000], [1, 1], 8, 32, 50, 0),
+    ([4, 12000], [9, 4], 2, 1024, 0, 0)])
+def test_prompt_few_queries_over_a_long_cache(kvs, lens, new, G, page, window, sinks, H):
+    """Items split over the tokens they see and joined; pieces with nothing to see among them."""
+    k, v, table, n = ref.make(lens, G, page, seed=H + page)
+    cache = kvs.PagedKV(k, v, table, n)
+    assert kvs._lib.kvs_paged_prompt_workspace_size(len(lens), G, H, sum(new) + 3, cache.cap) > 0
+    cu = [0] + [int(x) for x in np.cumsum(new)]
+    T = cu[-1] + 3
+    q = torch.randn(T, G * H, D, device=DEV).to(torch.bfloat16)
+    q[cu[-1]:] = float("nan")
+    out = torch.full((T, G * H, D), 3.5, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((T, G * H), -7.25, device=DEV)
+    st = _status()
+    kvs.paged_prompt_attn(q, torch.tensor(cu, dtype=torch.int32, device=DEV), cache, window, sinks, out=out, lse=lse,
+                          dev_status=st)
+    ref.check_prompt(out, lse, q, cu, k, v, table, lens, window, sinks, SC, G)
+    assert bool((out[cu[-1]:] == 3.5).all()) and bool((lse[cu[-1]:] == -7.25).all()) and int(st) == 0
+
+
 def test_prompt_items_that_see_nothing(kvs):
     """Many queries in front of the first token, between items that see something."""
     lens, new, G, H = [3, 260, 0], [900, 260, 500], 8, 8

@@ -36,7 +36,7 @@ def test_cache_descriptor_checks(kvs, change, status):
     d = kvs.PagedDecodeArgsC(ref, 4096, 0, 4, 0, 0, 1.0, 4096, None, None, None)
     assert L.paged_decode_attn(ctypes.byref(d), 4096, 1 << 40, None, None) == status
     p = kvs.PagedPromptArgsC(ref, 4096, 1 << 20, 4096, 4, 4, 0, 0, 1.0, 4096, 1 << 20, None)
-    assert L.paged_prompt_attn(ctypes.byref(p), None, None) == status
+    assert L.paged_prompt_attn(ctypes.byref(p), 4096, 1 << 40, None, None) == status
     e = kvs.PagedEvictArgsC(ref, 4096, None, None, 8, 0, 0, 4096, None, 4096, 4096)
     assert L.kvs_paged_evict(ctypes.byref(e), 4096, 1 << 40, None, None) == status
     assert L.kvs_last_error()
@@ -46,7 +46,7 @@ def test_null_descriptors(kvs):
     L = kvs._lib
     assert L.kvs_paged_append(None, 4096, 4096, 256, None, 2, None, None, None, None, None) == kvs.KVS_EINVAL
     assert L.paged_decode_attn(None, None, 0, None, None) == kvs.KVS_EINVAL
-    assert L.paged_prompt_attn(None, None, None) == kvs.KVS_EINVAL
+    assert L.paged_prompt_attn(None, None, 0, None, None) == kvs.KVS_EINVAL
     assert L.kvs_paged_evict(None, None, 0, None, None) == kvs.KVS_EINVAL
 
 
@@ -89,7 +89,7 @@ def test_prompt_checks(kvs, change, status):
              out_ld=1024, lse=None)
     f.update(change)
     a = kvs.PagedPromptArgsC(*f.values())
-    assert kvs._lib.paged_prompt_attn(ctypes.byref(a), None, None) == status
+    assert kvs._lib.paged_prompt_attn(ctypes.byref(a), 4096, 1 << 40, None, None) == status
 
 
 @pytest.mark.parametrize("change,status", [
@@ -113,6 +113,17 @@ def test_workspace_checks(kvs):
     assert kvs._lib.kvs_paged_evict(ctypes.byref(a), None, 0, None, None) == kvs.KVS_EWORKSPACE
     assert kvs._lib.kvs_paged_evict(ctypes.byref(a), 4096, need - 1, None, None) == kvs.KVS_EWORKSPACE
     assert kvs._lib.kvs_paged_evict(ctypes.byref(a), 4104, 1 << 40, None, None) == kvs.KVS_EINVAL
+
+
+def test_prompt_workspace(kvs):
+    """Few queries over a long cache are split and need a workspace; many do not."""
+    kv = _kv(kvs, max_pages=4096, table_ld=4096)
+    need = kvs._lib.kvs_paged_prompt_workspace_size(2, 2, 4, 8, 65536)
+    assert need > 0 and kvs._lib.kvs_paged_prompt_workspace_size(2, 2, 4, 1 << 16, 65536) == 0
+    assert kvs._lib.kvs_paged_prompt_workspace_size(2, 2, 4, 8, 128) == 0
+    a = kvs.PagedPromptArgsC(ctypes.pointer(kv), 4096, 1024, 4096, 8, 4, 0, 0, 1.0, 4096, 1024, None)
+    for ws, size, status in ((None, 0, kvs.KVS_EWORKSPACE), (4096, need - 1, kvs.KVS_EWORKSPACE), (4104, need, kvs.KVS_EINVAL)):
+        assert kvs._lib.paged_prompt_attn(ctypes.byref(a), ws, size, None, None) == status
 
 
 def test_binding_refuses_host_tensors(kvs):
