@@ -529,9 +529,9 @@ KVS_API size_t kvs_paged_decode_workspace_size(int32_t R, int32_t G, int32_t H, 
  * tokens at a time: a cached V row that is not finite makes the outputs of the
  * queries that see it not finite, and may those of other queries taken with
  * one that does; K and V rows that none of them sees have no influence on them.
- * Workspace: kvs_paged_prompt_workspace_size(R, G, H, T, max_pages * page), which
- * is 0 where there are queries enough to occupy the GPU; fewer are split over the
- * tokens they see, and the parts joined. */
+ * Workspace: kvs_paged_prompt_workspace_size(R, G, H, T, max_pages * page, window,
+ * sinks), which is 0 where there are queries enough to occupy the GPU; fewer are
+ * split over the tokens they see, and the parts joined. */
 typedef struct {
   const kvs_paged_kv* kv;
   const uint16_t* q;
@@ -546,7 +546,8 @@ typedef struct {
 
 KVS_API kvs_status paged_prompt_attn(const kvs_paged_prompt_args* a, void* ws, size_t ws_bytes,
                                      int32_t* dev_status, void* stream);
-KVS_API size_t kvs_paged_prompt_workspace_size(int32_t R, int32_t G, int32_t H, int32_t T, int32_t cap);
+KVS_API size_t kvs_paged_prompt_workspace_size(int32_t R, int32_t G, int32_t H, int32_t T, int32_t cap,
+                                               int32_t window, int32_t sinks);
 
 /* kvs_paged_evict -- cuts every request that holds more than `budget` tokens
  * down to `budget`, for each KV head by itself. Of the n[r] slots it keeps

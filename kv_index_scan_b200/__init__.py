@@ -130,7 +130,7 @@ def _declare():
     L.kvs_paged_decode_workspace_size.restype = SZ
     L.paged_prompt_attn.argtypes = [ctypes.POINTER(PagedPromptArgsC), P, SZ, P, P]
     L.paged_prompt_attn.restype = I32
-    L.kvs_paged_prompt_workspace_size.argtypes = [I32, I32, I32, I32, I32]
+    L.kvs_paged_prompt_workspace_size.argtypes = [I32] * 7
     L.kvs_paged_prompt_workspace_size.restype = SZ
     L.kvs_paged_evict.argtypes = [ctypes.POINTER(PagedEvictArgsC), P, SZ, P, P]
     L.kvs_paged_evict.restype = I32
@@ -754,7 +754,8 @@ def paged_prompt_attn(q: torch.Tensor, cu: torch.Tensor, cache: PagedKV, window:
     a = PagedPromptArgsC(cache._ref, q.data_ptr(), ld[0], cu.data_ptr(), T, Hq // cache.G, window, sinks,
                          1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), ld[1], lse.data_ptr())
     if ws is None:
-        ws = cache._workspace("kvs_paged_prompt_workspace_size", Hq // cache.G, T, cache.cap)
+        ws = cache._workspace("kvs_paged_prompt_workspace_size", Hq // cache.G, T, cache.cap, window,
+                              sinks)
     else:
         _check_ws(ws, dev)
     if ws is None:

@@ -107,8 +107,9 @@ kvs_status paged_decode_attn(const kvs_paged_decode_args* a, void* ws, size_t ws
   return ok();
 }
 
-size_t kvs_paged_prompt_workspace_size(int32_t R, int32_t G, int32_t H, int32_t T, int32_t cap) {
-  return paged_prompt_ws_bytes(R, G, H, T, cap);
+size_t kvs_paged_prompt_workspace_size(int32_t R, int32_t G, int32_t H, int32_t T, int32_t cap, int32_t window,
+                                       int32_t sinks) {
+  return paged_prompt_ws_bytes(R, G, H, T, cap, window, sinks);
 }
 
 kvs_status paged_prompt_attn(const kvs_paged_prompt_args* a, void* ws, size_t ws_bytes, int32_t* dev_status,
@@ -127,7 +128,8 @@ kvs_status paged_prompt_attn(const kvs_paged_prompt_args* a, void* ws, size_t ws
   KVS_REQUIRE(static_cast<int64_t>(a->T) * a->H < (1ll << 31) - 4096, KVS_EUNSUPPORTED,
               "paged_prompt_attn: T*H=%lld rows (below 2^31)", static_cast<long long>(a->T) * a->H);
   KVS_REQUIRE(aligned16(a->q) && aligned16(a->out), KVS_EINVAL, "paged_prompt_attn: q and out must be 16-byte aligned");
-  const size_t need = paged_prompt_ws_bytes(a->kv->R, a->kv->G, a->H, a->T, a->kv->max_pages * a->kv->page);
+  const size_t need = paged_prompt_ws_bytes(a->kv->R, a->kv->G, a->H, a->T, a->kv->max_pages * a->kv->page, a->window,
+                                           a->sinks);
   KVS_REQUIRE(need == 0 || (ws && ws_bytes >= need), KVS_EWORKSPACE, "paged_prompt_attn: workspace %zu < %zu bytes",
               ws_bytes, need);
   KVS_REQUIRE(aligned16(ws), KVS_EINVAL, "paged_prompt_attn: the workspace must be 16-byte aligned");

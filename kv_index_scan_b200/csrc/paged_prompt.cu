@@ -60,7 +60,7 @@ constexpr int kThreads = 32 * 12;             // three warpgroups
 // registers a thread: 168 at launch; 8 * 208 + 4 * 88 = 12 * 168
 constexpr int kSoftRegs = 208, kOtherRegs = 88;
 constexpr int kMaxPieces = 32;               // of an item (a lane of the join each)
-constexpr int kPieceTiles = 8;               // of the longest request, at least (1024 tokens: 20.6 us whole, 23.1 in two)
+constexpr int kPieceTiles = 4;               // that a piece has at least
 constexpr float kGrow = 8.f;                 // log2 of the growth that a maximum may lag behind
 
 struct PromptSmem {
@@ -287,9 +287,11 @@ __device__ __forceinline__ bool find_item(const PromptParams& p, uint32_t x, Ite
       }
       it.tiles = it.nsink + (it.end + kTok - 1) / kTok - it.first;
       if constexpr (kPieces) {
+        // no more pieces than have kPieceTiles tiles each; the others are empty
+        const int pieces = max(1, min(p.pieces, it.tiles / kPieceTiles)), at = min(it.piece, pieces);
         const int64_t tiles = it.tiles;
-        it.from = static_cast<int>(tiles * it.piece / p.pieces);
-        it.tiles = static_cast<int>(tiles * (it.piece + 1) / p.pieces) - it.from;
+        it.from = static_cast<int>(tiles * at / pieces);
+        it.tiles = static_cast<int>(tiles * min(at + 1, pieces) / pieces) - it.from;
       }
       return true;
     }
@@ -770,22 +772,36 @@ __global__ void __launch_bounds__(256) paged_prompt_join_kernel(const PromptPara
   if (p.lse && lane == 0) p.lse[row] = L == 0.f ? ninf : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-// No more items than this, whatever the lengths: a part item a request, and whole ones.
+// No more items than this, whatever the lengths: each request's last one may be
+// part empty.
 int64_t most_items(int R, int G, int H, int T) {
-  const int per2 = 2 * (kRows / H);
-  return (T / per2 + static_cast<int64_t>(T < R ? T : R)) * G;
+  const int64_t per2 = 2 * (kRows / H);
+  return (T + (T < R ? T : R) * (per2 - 1)) / per2 * G;
 }
 
-// Pieces that an item's tiles are split in: as many as give every SM one where
-// the items do not, of at least kPieceTiles tiles of the longest request.
-int pieces_of(int R, int G, int H, int T, int64_t cap) {
-  const int64_t items = most_items(R, G, H, T);
-  if (items <= 0) return 1;
-  int64_t n = sm_count() / items;
-  if (n > kMaxPieces) n = kMaxPieces;
-  const int64_t most = (cap + kTok - 1) / kTok / kPieceTiles;
-  if (n > most) n = most;
-  return n < 1 ? 1 : static_cast<int>(n);
+// Pieces that an item's tiles are split in. In units of a tile's time (1.75 us),
+// with t tiles in the longest item that there may be, a round of whole items
+// takes t + 3.5, one of n pieces t / n + 5, and the join 4 (8 heads, 4 tokens over
+// 28676: 359 us whole, 37 in 18 pieces; 2 heads, 1024 tokens: 20.6 whole, 23.1 in
+// two): the number with the least sum of rounds.
+int pieces_of(int R, int G, int H, int T, int64_t cap, int window, int sinks) {
+  const int64_t items = most_items(R, G, H, T), sms = sm_count();
+  int64_t t = (cap + kTok - 1) / kTok;
+  if (window) {
+    const int64_t seen = (static_cast<int64_t>(window) + 2 * (kRows / H) + kTok - 1) / kTok + 1 +
+                         (static_cast<int64_t>(sinks) + kTok - 1) / kTok;
+    if (seen < t) t = seen;
+  }
+  int best = 1;
+  double least = static_cast<double>((items + sms - 1) / sms) * (t + 3.5);
+  for (int n = 2; n <= kMaxPieces && n * kPieceTiles <= t; ++n) {
+    const double cost = static_cast<double>((items * n + sms - 1) / sms) * (static_cast<double>(t) / n + 5) + 4;
+    if (cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
 }
 
 size_t carve(PromptParams* p, void* ws, int G, int H, int T, int pieces) {
@@ -803,9 +819,9 @@ size_t carve(PromptParams* p, void* ws, int G, int H, int T, int pieces) {
 
 }  // namespace
 
-size_t paged_prompt_ws_bytes(int R, int G, int H, int T, int cap) {
+size_t paged_prompt_ws_bytes(int R, int G, int H, int T, int cap, int window, int sinks) {
   if (R < 1 || G < 1 || H < 1 || H > 8 || T < 1) return 0;
-  return carve(nullptr, nullptr, G, H, T, pieces_of(R, G, H, T, cap));
+  return carve(nullptr, nullptr, G, H, T, pieces_of(R, G, H, T, cap, window, sinks));
 }
 
 kvs_status paged_prompt_launch(const kvs_paged_prompt_args* a, void* ws, int32_t* dev_status, cudaStream_t s) {
@@ -828,7 +844,8 @@ kvs_status paged_prompt_launch(const kvs_paged_prompt_args* a, void* ws, int32_t
   KVS_PROPAGATE(paged_tensor_map(&mk, a->kv->K, p.kv, box, 1, "paged_prompt_attn"));
   KVS_PROPAGATE(paged_tensor_map(&mv, a->kv->V, p.kv, box, 1, "paged_prompt_attn"));
   KVS_PROPAGATE(query_tensor_map(&mq, a, p.per));
-  p.pieces = pieces_of(p.kv.R, p.kv.G, p.H, p.T, static_cast<int64_t>(a->kv->max_pages) * a->kv->page);
+  p.pieces = pieces_of(p.kv.R, p.kv.G, p.H, p.T, static_cast<int64_t>(a->kv->max_pages) * a->kv->page, p.window,
+                       p.sinks);
   carve(&p, ws, p.kv.G, p.H, p.T, p.pieces);
   const int64_t items = most_items(p.kv.R, p.kv.G, p.H, p.T) * p.pieces;
   KVS_REQUIRE(items < (1ll << 31) - (1 << 20), KVS_EUNSUPPORTED, "paged_prompt_attn: T=%d queries of G=%d KV heads", a->T,

@@ -385,7 +385,8 @@ def test_prompt_few_queries_over_a_long_cache(kvs, lens, new, G, page, window, s
     """Items split over the tokens they see and joined; pieces with nothing to see among them."""
     k, v, table, n = ref.make(lens, G, page, seed=H + page)
     cache = kvs.PagedKV(k, v, table, n)
-    assert kvs._lib.kvs_paged_prompt_workspace_size(len(lens), G, H, sum(new) + 3, cache.cap) > 0
+    assert (kvs._lib.kvs_paged_prompt_workspace_size(len(lens), G, H, sum(new) + 3, cache.cap, window, sinks) > 0) \
+        == (window != 50)
     cu = [0] + [int(x) for x in np.cumsum(new)]
     T = cu[-1] + 3
     q = torch.randn(T, G * H, D, device=DEV).to(torch.bfloat16)

@@ -118,9 +118,10 @@ def test_workspace_checks(kvs):
 def test_prompt_workspace(kvs):
     """Few queries over a long cache are split and need a workspace; many do not."""
     kv = _kv(kvs, max_pages=4096, table_ld=4096)
-    need = kvs._lib.kvs_paged_prompt_workspace_size(2, 2, 4, 8, 65536)
-    assert need > 0 and kvs._lib.kvs_paged_prompt_workspace_size(2, 2, 4, 1 << 16, 65536) == 0
-    assert kvs._lib.kvs_paged_prompt_workspace_size(2, 2, 4, 8, 128) == 0
+    need = kvs._lib.kvs_paged_prompt_workspace_size(2, 2, 4, 8, 65536, 0, 0)
+    assert need > 0 and kvs._lib.kvs_paged_prompt_workspace_size(2, 2, 4, 1 << 16, 65536, 0, 0) == 0
+    assert kvs._lib.kvs_paged_prompt_workspace_size(2, 2, 4, 8, 128, 0, 0) == 0
+    assert kvs._lib.kvs_paged_prompt_workspace_size(2, 2, 4, 8, 65536, 200, 4) == 0  # a short window
     a = kvs.PagedPromptArgsC(ctypes.pointer(kv), 4096, 1024, 4096, 8, 4, 0, 0, 1.0, 4096, 1024, None)
     for ws, size, status in ((None, 0, kvs.KVS_EWORKSPACE), (4096, need - 1, kvs.KVS_EWORKSPACE), (4104, need, kvs.KVS_EINVAL)):
         assert kvs._lib.paged_prompt_attn(ctypes.byref(a), ws, size, None, None) == status
