@@ -35,8 +35,9 @@
 // 0.50 ms by the clocks that the power cap leaves (1.10 to 1.25 PFLOP/s; a large
 // library product reaches 1.66 in a burst and 1.40 for seconds); 2048 tokens over
 // 32768 with a window of 4096: 144 us (0.96 PFLOP/s; 256 items for 148 SMs); 128
-// tokens 10 us. The products with their loads alone take 0.32 and 0.09 ms: what
-// is left is each row tile's chain from S through the softmax to the next S.
+// tokens 10 us; 4 tokens over 28676 37 us (359 before the split). The products
+// with their loads alone take 0.32 and 0.09 ms: what is left is each row tile's
+// chain from S through the softmax to the next S.
 // Every wait is bounded; one that runs out writes KVS_ETIMEOUT, and the block
 // winds down with no copy in flight and its tensor memory freed.
 #include <cuda_bf16.h>

@@ -400,6 +400,38 @@ def test_prompt_few_queries_over_a_long_cache(kvs, lens, new, G, page, window, s
     assert bool((out[cu[-1]:] == 3.5).all()) and bool((lse[cu[-1]:] == -7.25).all()) and int(st) == 0
 
 
+def test_prompt_pieces_in_a_graph_and_on_two_streams(kvs):
+    """A split call captured, and replayed after the lengths, offsets and queries changed in place (down to
+    caches of fewer tiles than pieces); two at once, each with its own workspace."""
+    lens = [9000, 6000]
+    k, v, table, n = ref.make(lens, 2, 64, seed=31, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    cu = torch.tensor([0, 4, 7], dtype=torch.int32, device=DEV)
+    q = torch.randn(8, 8, D, device=DEV).to(torch.bfloat16)
+    out, lse = torch.zeros(8, 8, D, dtype=torch.bfloat16, device=DEV), torch.zeros(8, 8, device=DEV)
+    kvs.paged_prompt_attn(q, cu, cache)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvs.paged_prompt_attn(q, cu, cache, out=out, lse=lse)
+    for m, c in ((lens, [0, 4, 7]), ([300, 8], [0, 1, 8]), ([5000, 0], [0, 8, 8]), ([0, 1], [0, 0, 1])):
+        n.copy_(torch.tensor(m))
+        cu.copy_(torch.tensor(c))
+        q.normal_()
+        graph.replay()
+        ref.check_prompt(out, lse, q, c, k, v, table, m, 0, 0, SC, 2)
+    n.copy_(torch.tensor(lens))
+    qs = [torch.randn(6, 8, D, device=DEV).to(torch.bfloat16) for _ in range(2)]
+    cu.copy_(torch.tensor([0, 2, 6]))
+    want = [kvs.paged_prompt_attn(x, cu, cache) for x in qs]
+    side = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[kvs.paged_prompt_attn(x, cu, cache, stream=s) for x, s in zip(qs, side)] for _ in range(10)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for (o, l), (wo, wl) in zip(pair, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
 def test_prompt_items_that_see_nothing(kvs):
     """Many queries in front of the first token, between items that see something."""
     lens, new, G, H = [3, 260, 0], [900, 260, 500], 8, 8
