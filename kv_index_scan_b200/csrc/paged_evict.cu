@@ -42,7 +42,7 @@ constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kKeysMost = 22 * 1024;  // keys of a block in shared memory (two blocks share an SM)
 constexpr int kFlight = 4;            // rows that a warp copies at a time (8: registers spill, 82 us for 68)
-constexpr int kRunLeast = 4096;       // slots of the longest row that a block takes at least
+constexpr int kFewMoves = 512, kRunFew = 4096, kRunMany = 2048;
 constexpr int kBatch = 8;             // slots that a thread reads at a time
 
 constexpr uint32_t kSure = 0xFFFFFFFFu;  // key of a protected slot
@@ -340,13 +340,17 @@ kvs_status paged_evict_launch(const kvs_paged_evict_args* a, void* ws, int32_t* 
   p.holes = static_cast<int32_t*>(ws);
   p.movers = p.holes + static_cast<size_t>(RG) * a->budget;
   p.dev_status = dev_status;
-  // blocks a row: enough to occupy two on every SM, each with at least
-  // kRunLeast slots of the longest row there may be. (128 rows of 4097 slots: one
-  // block a row 14.8 us, two 18.4: the cluster's barriers cost more than half a
-  // run saves. 64 rows of 16K to 64K slots: 82 us with four blocks a row.)
+  // blocks a row: enough to occupy two on every SM, each with at least so many
+  // slots of the longest row there may be. Where few rows can move, the cluster's
+  // barriers cost more than half a run saves (128 rows of 4097 slots, budget 4096:
+  // one block a row 13.8 us, two 17.7); where many can, the moves want the blocks
+  // (2 rows of 8765 slots cut to 1409: two blocks a row 21.4 us, four 14.8; 8 rows
+  // of 8192 cut to 4096: 29.5 and 22.7).
   const int64_t cap = static_cast<int64_t>(a->kv->max_pages) * a->kv->page;
+  const int64_t moves = cap - a->budget < a->budget ? cap - a->budget : a->budget;
+  const int64_t run = moves < kFewMoves ? kRunFew : kRunMany;
   int C = 1;
-  while (C < kMaxCluster && static_cast<int64_t>(RG) * C * 2 <= 2 * sm_count() && cap / (2 * C) >= kRunLeast) C *= 2;
+  while (C < kMaxCluster && static_cast<int64_t>(RG) * C * 2 <= 2 * sm_count() && cap / (2 * C) >= run) C *= 2;
   const int64_t most = (cap + C - 1) / C;
   p.keys_room = static_cast<int>(most < kKeysMost ? most : kKeysMost);
   const size_t smem = static_cast<size_t>(p.keys_room) * sizeof(uint32_t);
