@@ -29,7 +29,7 @@
 //    log-sum-exp is known.
 // Measured: 16 requests of 16K to 128K tokens, 3.70 GB: 0.54 to 0.62 ms (5.99 to
 // 6.9 TB/s of the 6.55 a copy reaches); 32 requests seeing 4100 tokens each, 8
-// heads: 88 us (5.7 TB/s); one request of 4096 tokens: 11.1 us, 3 of them the join.
+// heads: 88 us (5.7 TB/s); one request of 4096 tokens: 10.8 us, 2.5 of them the join.
 #include <cuda_bf16.h>
 
 #include "async.cuh"
@@ -527,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
 constexpr int kJoinThreads = 512;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kFewBatch = 8;
+constexpr int kCutThreads = 256;  // with 77 registers a thread three blocks an SM
 constexpr int kJoinTokens = 2048;  // tokens of a row that one block turns into weights
 
 // Parts way, way + ways, ... of a head, their maximum M, sum L and output acc
@@ -618,28 +619,14 @@ struct Parts {
   }
 };
 
-// Row u's parts joined, for no more rows than SMs (each then has many parts):
-// one round of loads, eight parts of a head in flight a warp, and the warps'
-// sums meet in shared memory. One row of 4096 tokens: the whole call 11.1 us,
-// 12.5 with the kernel below; 256 rows 90.4 us, 88.4 with the one below (its
-// registers leave room for one block an SM).
-__global__ void __launch_bounds__(kJoinThreads) paged_decode_join_few_kernel(const DecodeParams p) {
-  __shared__ int64_t scan_part[2][kJoinWarps];
-  __shared__ float s_sum[kJoinWarps][kD];
-  __shared__ float s_ml[kJoinWarps][2];
+// Row u's parts, of blocks b0 to b1, joined: one round of loads, eight parts of a
+// head in flight a warp, and the warps' sums meet in shared memory.
+template <int kT>
+__device__ __forceinline__ void join_row(const DecodeParams& p, int u, int b0, int b1, float (&s_sum)[kT / 32][kD],
+                                         float (&s_ml)[kT / 32][2]) {
   const float ninf = -__int_as_float(0x7f800000);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int u = blockIdx.x, r = u / p.kv.G, g = u % p.kv.G, H = p.H;
-  const VisibleTiles<kUnit> vt(p.kv.length(r, nullptr), p.window, p.sinks);
-  int b0, b1;
-  blocks_of_row<kJoinThreads>(p, r, g, vt, scan_part, b0, b1);
-  pdl_wait();
-  if (vt.count == 0) {
-    write_nothing(p, u);
-    return;
-  }
-  if (b0 == b1) return;
-  const int shift = H <= 1 ? 0 : (H <= 2 ? 1 : (H <= 4 ? 2 : 3)), heads = 1 << shift, ways = kJoinWarps >> shift;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, H = p.H;
+  const int shift = H <= 1 ? 0 : (H <= 2 ? 1 : (H <= 4 ? 2 : 3)), heads = 1 << shift, ways = (kT / 32) >> shift;
   const int h = warp & (heads - 1), way = warp >> shift;
   if (h < H) {
     float M, L;
@@ -652,7 +639,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_few_kernel(con
     *reinterpret_cast<float4*>(&s_sum[warp][4 * lane]) = acc;
   }
   __syncthreads();
-  for (int e = tid; e < H * kD; e += kJoinThreads) {
+  for (int e = tid; e < H * kD; e += kT) {
     const int eh = e / kD;
     float M = ninf, L = 0.f, o = 0.f;
     for (int w = 0; w < ways; ++w) M = fmaxf(M, s_ml[w * heads + eh][0]);
@@ -668,9 +655,70 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_few_kernel(con
   }
 }
 
+// A block for every row, for no more rows than SMs (each then has many parts).
+// The whole call, and with the kernel below: 8 rows of 4096 tokens 10.5 us, 12.3;
+// 128 rows of 4096 tokens 49.6 us, 50.5; 160 rows 61.0 us either way.
+__global__ void __launch_bounds__(kJoinThreads) paged_decode_join_few_kernel(const DecodeParams p) {
+  __shared__ int64_t scan_part[2][kJoinWarps];
+  __shared__ float s_sum[kJoinWarps][kD];
+  __shared__ float s_ml[kJoinWarps][2];
+  const int u = blockIdx.x, r = u / p.kv.G, g = u % p.kv.G;
+  const VisibleTiles<kUnit> vt(p.kv.length(r, nullptr), p.window, p.sinks);
+  int b0, b1;
+  blocks_of_row<kJoinThreads>(p, r, g, vt, scan_part, b0, b1);
+  pdl_wait();
+  if (vt.count == 0)
+    write_nothing(p, u);
+  else if (b0 != b1)
+    join_row<kJoinThreads>(p, u, b0, b1, s_sum, s_ml);
+}
+
+// A block for every end of a block's run, for more rows than SMs: fewer runs end
+// than there are rows, and most rows lie in one run and need no joining. Block b
+// joins the row that run b ends in the middle of, if the row begins in run b, and
+// sees to every gridDim.x-th of the requests that nothing is seen of. 4096 rows of
+// 256 tokens: the whole call 103 us, with a block for every row 129; 1024 rows of
+// 1024 tokens 92 us, 99.
+__global__ void __launch_bounds__(kCutThreads) paged_decode_join_cut_kernel(const DecodeParams p) {
+  __shared__ int64_t scan_part[kCutThreads / 32];
+  __shared__ float s_sum[kCutThreads / 32][kD];
+  __shared__ float s_ml[kCutThreads / 32][2];
+  __shared__ int s_u, s_b1;
+  const PagedView& kv = p.kv;
+  const int tid = threadIdx.x, b = blockIdx.x;
+  const int own = (kv.R + kCutThreads - 1) / kCutThreads, r0 = min(kv.R, own * tid), r1 = min(kv.R, r0 + own);
+  int64_t mine = 0, U;
+  for (int r = r0; r < r1; ++r) mine += VisibleTiles<kUnit>(kv.length(r, nullptr), p.window, p.sinks).count;
+  if (tid == 0) s_u = -1;
+  int64_t base = block_scan<kCutThreads>(mine, scan_part, U) * kv.G;
+  U *= kv.G;
+  const int nb = sharing(U, p.blocks);
+  if (b + 1 < nb) {
+    const int64_t x = first_unit(U, b + 1, nb);  // the first unit of the next run
+    if (x > base && x < base + mine * kv.G) {
+      int64_t count = 0;
+      for (int r = r0; r < r1; ++r, base += count * kv.G) {
+        count = VisibleTiles<kUnit>(kv.length(r, nullptr), p.window, p.sinks).count;
+        if (x >= base + count * kv.G) continue;
+        const int64_t g = (x - base) / count, begin = base + g * count;
+        if (begin < x && block_of_unit(U, begin, nb) == b) {
+          s_u = r * kv.G + static_cast<int>(g);
+          s_b1 = block_of_unit(U, begin + count - 1, nb);
+        }
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  pdl_wait();
+  for (int r = b; r < kv.R; r += gridDim.x)
+    if (VisibleTiles<kUnit>(kv.length(r, nullptr), p.window, p.sinks).count == 0)
+      for (int g = 0; g < kv.G; ++g) write_nothing(p, r * kv.G + g);
+  if (s_u >= 0) join_row<kCutThreads>(p, s_u, b, s_b1, s_sum, s_ml);
+}
+
 // Row u's parts joined (block x = 0 of the row), and its weights (every block).
-template <bool kWeights>
-__global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const DecodeParams p, int chunks) {
+__global__ void __launch_bounds__(kJoinThreads) paged_decode_weights_kernel(const DecodeParams p, int chunks) {
   __shared__ int64_t scan_part[2][kJoinWarps];
   __shared__ float s_lse2[8];
   __shared__ float s_sum[kJoinWarps][kD];
@@ -689,7 +737,6 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const D
     return;
   }
   if (b0 == b1) {
-    if (!kWeights) return;
     if (tid < H) s_lse2[tid] = p.lse2[static_cast<size_t>(u) * H + tid];
   } else {
     // a head's parts are dealt to `ways` warps, each of which finds their maximum and
@@ -743,35 +790,33 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const D
         p.out[static_cast<size_t>(u) * H * kD + e] = o;
       }
   }
-  if constexpr (kWeights) {
-    __syncthreads();
-    const size_t row = static_cast<size_t>(u) * kv.cap();
-    float z[8];
+  __syncthreads();
+  const size_t row = static_cast<size_t>(u) * kv.cap();
+  float z[8];
 #pragma unroll
-    for (int h = 0; h < 8; ++h) z[h] = h < H ? s_lse2[h] : ninf;
+  for (int h = 0; h < 8; ++h) z[h] = h < H ? s_lse2[h] : ninf;
 #pragma unroll
-    for (int e = tid; e < kJoinTokens; e += kJoinThreads) {
-      const int k = chunk * (kJoinTokens / kUnit) + e / kUnit;
-      if (k >= vt.count) break;
-      const int t = vt.tile(k) * kUnit + e % kUnit;
-      if (t >= vt.end || (t < vt.lo && t >= p.sinks)) continue;
-      const float* l = p.logits + (row + t) * p.hp;
-      const float m = p.mass[row + t];
-      float w = 0.f;
-      auto add = [&](float x, int h) { w += z[h] == ninf ? 0.f : exp2f(x - z[h]); };
-      if (p.hp == 2) {
-        const float2 v = *reinterpret_cast<const float2*>(l);
-        add(v.x, 0), add(v.y, 1);
-      } else {
-        const float4 v = *reinterpret_cast<const float4*>(l);
-        add(v.x, 0), add(v.y, 1), add(v.z, 2), add(v.w, 3);
-        if (p.hp == 8) {
-          const float4 y = *reinterpret_cast<const float4*>(l + 4);
-          add(y.x, 4), add(y.y, 5), add(y.z, 6), add(y.w, 7);
-        }
+  for (int e = tid; e < kJoinTokens; e += kJoinThreads) {
+    const int k = chunk * (kJoinTokens / kUnit) + e / kUnit;
+    if (k >= vt.count) break;
+    const int t = vt.tile(k) * kUnit + e % kUnit;
+    if (t >= vt.end || (t < vt.lo && t >= p.sinks)) continue;
+    const float* l = p.logits + (row + t) * p.hp;
+    const float m = p.mass[row + t];
+    float w = 0.f;
+    auto add = [&](float x, int h) { w += z[h] == ninf ? 0.f : exp2f(x - z[h]); };
+    if (p.hp == 2) {
+      const float2 v = *reinterpret_cast<const float2*>(l);
+      add(v.x, 0), add(v.y, 1);
+    } else {
+      const float4 v = *reinterpret_cast<const float4*>(l);
+      add(v.x, 0), add(v.y, 1), add(v.z, 2), add(v.w, 3);
+      if (p.hp == 8) {
+        const float4 y = *reinterpret_cast<const float4*>(l + 4);
+        add(y.x, 4), add(y.y, 5), add(y.z, 6), add(y.w, 7);
       }
-      p.mass_out[row + t] = m + w;
     }
+    p.mass_out[row + t] = m + w;
   }
 }
 
@@ -801,11 +846,13 @@ kvs_status launch(const DecodeParams& p, const CUtensorMap& mk, const CUtensorMa
   allow_smem<paged_decode_kernel<kF32Q, kWeights>>(sizeof(DecodeSmem));
   launch_chained(paged_decode_kernel<kF32Q, kWeights>, dim3(p.blocks), dim3(kThreads), sizeof(DecodeSmem), s, p, mk,
                  mv);
-  if (!kWeights && joins <= sm_count())
-    launch_chained(paged_decode_join_few_kernel, dim3(static_cast<unsigned>(joins)), dim3(kJoinThreads), 0, s, p);
+  const dim3 rows(static_cast<unsigned>(joins));
+  if (kWeights)
+    launch_chained(paged_decode_weights_kernel, rows, dim3(kJoinThreads), 0, s, p, static_cast<int>(chunks));
+  else if (joins <= sm_count())
+    launch_chained(paged_decode_join_few_kernel, rows, dim3(kJoinThreads), 0, s, p);
   else
-    launch_chained(paged_decode_join_kernel<kWeights>, dim3(static_cast<unsigned>(joins)), dim3(kJoinThreads), 0, s, p,
-                   static_cast<int>(chunks));
+    launch_chained(paged_decode_join_cut_kernel, dim3(p.blocks), dim3(kCutThreads), 0, s, p);
   return check_launch("paged_decode_attn");
 }
 

@@ -199,6 +199,30 @@ def test_decode_one_long_row_among_many(kvs, H, weights):
     ref.check_decode(out, lse, q, k, v, table, lens, 0, 0, SC, torch.zeros_like(mass) if weights else None, mass)
 
 
+@pytest.mark.parametrize("R,G,H,window,sinks", [(700, 2, 4, 0, 0), (300, 1, 8, 0, 0), (1100, 1, 3, 40, 9), (40, 8, 2, 0, 0)])
+def test_decode_many_short_rows(kvs, R, G, H, window, sinks):
+    """More rows than blocks: empty ones, ones within a block's run, ones cut once."""
+    rng = np.random.default_rng(R)
+    lens = [int(x) for x in rng.integers(1, 400, R)]
+    for i in range(0, R, 3):
+        lens[i] = 0
+    k, v, table, n = ref.make(lens, G, 16, seed=R, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(R, G, H, D, device=DEV)
+    out = torch.full((R, G, H, D), float("nan"), device=DEV)
+    lse = torch.full((R, G, H), float("nan"), device=DEV)
+    out, lse = kvs.paged_decode_attn(q, cache, window, sinks, out=out, lse=lse)
+    ref.check_decode(out, lse, q, k, v, table, lens, window, sinks, SC)
+
+
+@pytest.mark.parametrize("R", [1, 200, 600])
+def test_decode_nothing_seen(kvs, R):
+    k, v, table, n = ref.make([0] * R, 2, 16, seed=R, poison=False)
+    q = torch.randn(R, 2, 4, D, device=DEV)
+    out, lse = kvs.paged_decode_attn(q, kvs.PagedKV(k, v, table, n), out=torch.full((R, 2, 4, D), 7.0, device=DEV))
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+
+
 def test_decode_extreme_logits(kvs):
     """Logits from -3e4 to 3e4 and equal ones: the running maximum carries every one."""
     lens = [700, 700]
