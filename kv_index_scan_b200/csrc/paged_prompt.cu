@@ -35,13 +35,14 @@
 // 0.50 ms by the clocks that the power cap leaves (1.10 to 1.25 PFLOP/s; a large
 // library product reaches 1.66 in a burst and 1.40 for seconds); 2048 tokens over
 // 32768 with a window of 4096: 144 us (0.96 PFLOP/s; 256 items for 148 SMs); 128
-// tokens 10 us; 4 tokens over 28676 37 us (359 before the split). The products
+// tokens 9.4 us; 4 tokens over 28676 37 us (359 before the split). The products
 // with their loads alone take 0.32 and 0.09 ms: what is left is each row tile's
 // chain from S through the softmax to the next S.
 // Every wait is bounded; one that runs out writes KVS_ETIMEOUT, and the block
 // winds down with no copy in flight and its tensor memory freed.
 #include <cuda_bf16.h>
 
+#include <cstring>
 #include <type_traits>
 
 #include "async.cuh"
@@ -56,7 +57,9 @@ constexpr int kHalfBytes = 128 * 128;        // 128 rows of one 128-byte half
 constexpr int kTileBytes = 2 * kHalfBytes;   // 128 rows of 128 bf16
 constexpr int kStages = 2;                   // of K, and of V
 constexpr int kInfos = 4;
+constexpr int kItems = 4;                    // found ahead of the warps that work on them
 constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kCleanWarps = 2;
+constexpr int kTakers = kSoftWarps + 1 + kCleanWarps;  // warps that take items from the loads' warp
 constexpr int kThreads = 32 * 12;             // three warpgroups
 // registers a thread: 168 at launch; 8 * 208 + 4 * 88 = 12 * 168
 constexpr int kSoftRegs = 208, kOtherRegs = 88;
@@ -68,8 +71,10 @@ struct PromptSmem {
   alignas(1024) unsigned char q[2][kTileBytes];
   unsigned char k[kStages][kTileBytes];
   unsigned char v[kStages][kTileBytes];
-  unsigned char stage[kSoftWarps][32 * 64];  // outputs on their way
+  unsigned char stage[kSoftWarps][32 * 128];  // outputs on their way
+  int4 items[kItems][4];                     // the last word: whether it is an item
   uint64_t q_full, q_empty, k_full[kStages], k_empty[kStages], v_full[kStages], v_clean[kStages], v_empty[kStages];
+  uint64_t item_full[kItems], item_empty[kItems];
   uint64_t s_full[2], p_full[2][2], o_full[2], drain;  // p_full by tile and half of the tokens
   int groups[kInfos];                        // by tile: which 16-token groups were loaded
   uint32_t tmem;
@@ -237,9 +242,11 @@ struct Item {
 
 // Item x of all, found by the whole warp: its pieces innermost, then the KV heads,
 // the blocks of a request from its last (which sees most) to its first, the last request first.
-// False behind the last one.
+// False behind the last one. The search goes on where the last one (for a smaller
+// x) ended: below request top, with the items of the requests above it in base.
 template <bool kPieces>
-__device__ __forceinline__ bool find_item(const PromptParams& p, uint32_t x, Item<kPieces>& it) {
+__device__ __forceinline__ bool find_item(const PromptParams& p, uint32_t x, int& top, uint32_t& base,
+                                          Item<kPieces>& it) {
   const PagedView& kv = p.kv;
   const int lane = threadIdx.x & 31;
   uint32_t whole = x;
@@ -249,8 +256,7 @@ __device__ __forceinline__ bool find_item(const PromptParams& p, uint32_t x, Ite
   }
   const uint32_t order = whole / static_cast<uint32_t>(kv.G);
   it.g = static_cast<int>(whole - order * kv.G);
-  uint32_t base = 0;
-  for (int top = kv.R; top > 0; top -= 32) {
+  for (; top > 0; top -= 32) {
     const int r = top - 1 - lane;
     int q0 = 0, c = 0, n = 0;
     if (r >= 0) {
@@ -311,14 +317,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PagedView& kv = p.kv;
   const int G = kv.G, H = p.H;
-  // The block's items: one of each round of gridDim.x, in the order of the
-  // blocks and in the reverse in turn (items shrink along the order). Every warp
-  // finds them for itself.
-  uint32_t round = 0;
-  auto next_item = [&](Item<kPieces>& it) {
-    const uint32_t at = round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-    return find_item(p, round++ * gridDim.x + at, it);
-  };
 
   if (tid == 0) {
     mbar_init(&sm.q_full, 1);
@@ -337,6 +335,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
       mbar_init(&sm.p_full[i][1], kRows / 32);
       mbar_init(&sm.o_full[i], 1);
     }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&sm.item_full[i], 1);
+      mbar_init(&sm.item_empty[i], kTakers);
+    }
     sm.abort_flag = 0;
     mbar_init_fence();
     tma_prefetch_map(&mapQ);
@@ -350,8 +352,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
   }
   pdl_wait();
   pdl_trigger();
+  // The block's items: one of each round of gridDim.x, in the order of the
+  // blocks and in the reverse in turn (items shrink along the order). The loads'
+  // warp finds each while the tiles of the one before are under way, and hands it
+  // on through shared memory: finding one takes 1,500 cycles and more (3,000 with
+  // 148 requests), which every warp spent between two items when it found them for
+  // itself, from the first request on each time. 592 items of one tile took 46.6 us
+  // so and take 39; 592 of a window's six tiles 89 and 83; 512 requests of 17 tokens
+  // over 100 258 and 150.
+  uint32_t round = 0, base = 0;
+  int top = kv.R;
+  auto find = [&](Item<kPieces>& it) {
+    const uint32_t at = round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+    return find_item(p, round * gridDim.x + at, top, base, it);
+  };
   Item<kPieces> it;
-  bool more = next_item(it);
   fence_before();
   __syncthreads();
   fence_after();
@@ -373,6 +388,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
     if (__all_sync(0xFFFFFFFFu, mbar_try(b, parity))) return true;
     return __all_sync(0xFFFFFFFFu, wait(b, parity)) != 0;
   };
+  static_assert(sizeof(Item<kPieces>) < sizeof(sm.items[0]), "the last word is kept");
+  auto read_item = [&](uint32_t of, Item<kPieces>& it) {
+    int4 w[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) w[x] = sm.items[of % kItems][x];
+    memcpy(&it, w, sizeof(it));
+    return w[3].w != 0;
+  };
+  // by a whole warp other than the loads': the next item, false behind the last
+  auto take = [&](Item<kPieces>& it, bool& ok) {
+    const int slot = round % kItems;
+    ok = wait_all(&sm.item_full[slot], round / kItems & 1);
+    if (!ok) return false;
+    const bool is = read_item(slot, it);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.item_empty[slot]);
+    ++round;
+    return is;
+  };
   // In every role: `at` counts the tiles, and `live` the items that have any, of
   // the whole launch; a phase of a barrier belongs to one of them.
   int at = 0, live = 0;
@@ -385,22 +419,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
       const int box = min(1 << kv.shift, kTok), pages = kTok / box;
       const int half = lane & 1, sub = lane >> 1;
       int issued = 0;  // K and V tiles
-      for (; more && ok; more = next_item(it)) {
-        if (it.tiles > 0) {
-          int go = 1;
-          if (lane == 0) {
-            if (live > 0) go = wait(&sm.q_empty, (live - 1) & 1);
-            if (go) {
-              mbar_expect(&sm.q_full, 4 * p.per * H * 128);
-              for (int x = 0; x < 4; ++x)
-                tma_query_rows(sm_addr(sm.q[x >> 1]) + (x & 1) * kHalfBytes, &mapQ, it.g * H,
-                               it.q0 + it.tok0 + (x >> 1) * p.per, x & 1, &sm.q_full);
-            }
+      // the next item found and handed on
+      auto hand_on = [&] {
+        const int slot = round % kItems;
+        Item<kPieces> then;
+        const bool is = find(then);
+        int go = 1;
+        if (lane == 0) {
+          if (round >= kItems) go = wait(&sm.item_empty[slot], (round / kItems - 1) & 1);
+          if (go) {
+            int4 w[4] = {};
+            memcpy(w, &then, sizeof(then));
+            w[3].w = is;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sm.items[slot][x] = w[x];
+            mbar_arrive(&sm.item_full[slot]);
           }
-          ok = __shfl_sync(0xFFFFFFFFu, go, 0) != 0;
-          if (!ok) break;
-          ++live;
         }
+        ++round;
+        __syncwarp();
+        return __shfl_sync(0xFFFFFFFFu, go, 0) != 0;
+      };
+      ok = hand_on();
+      bool more = ok && read_item(0, it);
+      while (more && ok) {
         // this lane's page id of tile i, unchecked (nothing waits for it here); -1 where none is needed
         auto wanted = [&](int i) {
           const int t = it.token(i) + sub * box;
@@ -443,8 +485,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
               tma_page_rows(sm_addr(which ? sm.v[st] : sm.k[st]) + to, which ? &mapV : &mapK, in_page, half, it.g, id,
                             full);
             ++issued;
+            if (i == 0 && which == 0) {  // the queries after the first K tile, whose place is free before theirs
+              if (lane == 0) {
+                if (live > 0) go = wait(&sm.q_empty, (live - 1) & 1);
+                if (go) {
+                  mbar_expect(&sm.q_full, 4 * p.per * H * 128);
+                  for (int x = 0; x < 4; ++x)
+                    tma_query_rows(sm_addr(sm.q[x >> 1]) + (x & 1) * kHalfBytes, &mapQ, it.g * H,
+                                   it.q0 + it.tok0 + (x >> 1) * p.per, x & 1, &sm.q_full);
+                }
+              }
+              ok = __shfl_sync(0xFFFFFFFFu, go, 0) != 0;
+              live += ok;
+            }
           }
+          // the next item, with two tiles on their way
+          if (ok && i == min(1, it.tiles - 1)) ok = hand_on();
         }
+        if (ok && it.tiles <= 0) ok = hand_on();
+        more = ok && read_item(round - 1, it);
       }
       // no copy may be in flight when the block ends
       if (lane == 0 && live > 0) mbar_wait(&sm.q_full, (live - 1) & 1);
@@ -455,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
         }
     } else if (warp >= kCleanWarp) {
       // ---------------- rows of V that no row of the block sees ----------------
-      for (; more && ok; more = next_item(it)) {
+      while (ok && take(it, ok)) {
         for (int i = 0; i < it.tiles && ok; ++i, ++at) {
           const int st = at % kStages;
           ok = wait_all(&sm.v_full[st], (at / kStages) & 1);
@@ -501,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
       auto commit = [&](uint64_t* bar) {
         if (leader) mma_commit_to(bar);
       };
-      for (; more && ok; more = next_item(it)) {
+      while (ok && take(it, ok)) {
         if (it.tiles == 0) continue;
         ok = wait_all(&sm.q_full, live & 1) && wait_all(&sm.k_full[at % kStages], (at / kStages) & 1);
         if (!ok) break;
@@ -564,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
     // a multiplication); rows behind the tile's last token go with it
     const uint32_t by_h = 65536u / H + 1;
     auto token_of = [&](int x) { return min(static_cast<int>(x * by_h >> 16), p.per - 1); };
+    bool more = take(it, ok);
     while (more && ok) {
       const int pos = it.p_lo + t * p.per + token_of(tid & 127);
       // the first and last position of this warp's rows
@@ -653,77 +713,75 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
         unpair(add2(z[0], z[1]), z0, z1);
         l += z0 + z1;
       }
-      // the next item is found while this one's last products run
-      const Item<kPieces> was = it;
-      more = next_item(it);
       // ---------------- the rows' output ----------------
-      bool done = ok && was.tiles > 0;
-      if (done) {
-        done = ok = wait_all(&sm.o_full[t], live & 1);
-        ++live;
-      }
-      fence_after();
-      const float inv = !done ? 0.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
-      // whether row x of the tile is there, and its place among all rows
-      const int tok = was.tok0 + t * p.per;
-      auto there = [&](int x) { return x < p.per * H && tok + token_of(x) < was.c; };
-      auto token_row = [&](int x) { return static_cast<int64_t>(was.q0 + tok + token_of(x)); };
-      auto head_of = [&](int x) { return was.g * H + x - token_of(x) * H; };
+      // (what does not need the outputs comes before the wait for the last products)
+      const int tok = it.tok0 + t * p.per, x = tid & 127;
+      const bool there = x < p.per * H && tok + token_of(x) < it.c;  // whether this thread's row is there
+      const int64_t token_row = static_cast<int64_t>(it.q0 + tok + token_of(x));
+      const int head = it.g * H + x - token_of(x) * H;
+      const bool some = ok && it.tiles > 0;  // (the next item is taken before that wait too)
       if constexpr (kPieces) {
         // a part: the row as it is, for the join
-        const int64_t row = there(tid & 127)
-                                ? (was.piece * static_cast<int64_t>(p.T) + token_row(tid & 127)) * G * H + head_of(tid & 127)
-                                : -1;
-        if (row >= 0) p.part_ml[row] = done ? make_float2(m, l) : make_float2(ninf, 0.f);
+        const int64_t row = (it.piece * static_cast<int64_t>(p.T) + token_row) * G * H + head;
+        more = ok && take(it, ok);
+        const bool done = some && wait_all(&sm.o_full[t], live & 1);
+        ok = ok && done == some;
+        live += some;
+        fence_after();
+        if (there) p.part_ml[row] = done ? make_float2(m, l) : make_float2(ninf, 0.f);
 #pragma unroll 1
         for (int e = 0; e < 4 && done; ++e) {
           float o[32];
           tmem_ld32(o_at + 32 * e, o);
           wait_ld();
-          if (row >= 0) {
+          if (there) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
               *reinterpret_cast<float4*>(p.part_o + row * kD + 32 * e + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
           }
           __syncwarp();
         }
-        fence_before();
-        continue;
-      }
-      if (p.lse && there(tid & 127))
-        p.lse[token_row(tid & 127) * G * H + head_of(tid & 127)] =
-            l == 0.f ? ninf : (m + log2f(l)) * 0.6931471805599453f;
-      // 32 channels at a time (rounded to bf16 here) through 64 bytes a row of
-      // shared memory, 16-byte pieces exchanged so that neither side conflicts:
-      // four lanes write a row. (Not unrolled: code that runs once an item.)
-      unsigned char* stage = sm.stage[warp];
-      uint16_t* to[4];
+      } else {
+        if (p.lse && there)
+          p.lse[token_row * G * H + head] = l == 0.f ? ninf : (m + log2f(l)) * 0.6931471805599453f;
+        // 64 channels at a time (rounded to bf16 here) through 128 bytes a row of
+        // shared memory, 16-byte pieces exchanged so that neither side conflicts:
+        // eight lanes write a row. (Not unrolled: code that runs once an item.)
+        unsigned char* stage = sm.stage[warp];
+        const int64_t own = there ? token_row * p.out_ld + head * kD : -1;
+        int64_t to[8];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int row = w0 + 8 * x + (lane >> 2);
-        to[x] = there(row) ? p.out + token_row(row) * p.out_ld + head_of(row) * kD + 8 * (lane & 3) : nullptr;
-      }
+        for (int y = 0; y < 8; ++y) to[y] = __shfl_sync(0xFFFFFFFFu, own, 4 * y + (lane >> 3));
+        uint16_t* out = p.out + 8 * (lane & 7);
+        more = ok && take(it, ok);
+        const bool done = some && wait_all(&sm.o_full[t], live & 1);
+        ok = ok && done == some;
+        live += some;
+        fence_after();
+        const float inv = !done ? 0.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
 #pragma unroll 1
-      for (int e = 0; e < 4; ++e) {
-        float o[32];
-        tmem_ld32(o_at + 32 * e, o);
-        wait_ld();
+        for (int e = 0; e < 2; ++e) {
+          float o[64];
+          tmem_ld32(o_at + 64 * e, o);
+          tmem_ld32(o_at + 64 * e + 32, o + 32);
+          wait_ld();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint4 v = make_uint4(bf16_pair(o[8 * j] * inv, o[8 * j + 1] * inv), bf16_pair(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
-                               bf16_pair(o[8 * j + 4] * inv, o[8 * j + 5] * inv),
-                               bf16_pair(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
-          if (!done) v = make_uint4(0, 0, 0, 0);  // tensor memory that nothing was written to
-          *reinterpret_cast<uint4*>(stage + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = v;
-        }
-        __syncwarp();
+          for (int j = 0; j < 8; ++j) {
+            uint4 v = make_uint4(bf16_pair(o[8 * j] * inv, o[8 * j + 1] * inv), bf16_pair(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
+                                 bf16_pair(o[8 * j + 4] * inv, o[8 * j + 5] * inv),
+                                 bf16_pair(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
+            if (!done) v = make_uint4(0, 0, 0, 0);  // tensor memory that nothing was written to
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = v;
+          }
+          __syncwarp();
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int rr = 8 * x + (lane >> 2), j = lane & 3;
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((j ^ (rr >> 1 & 3)) << 4));
-          if (to[x]) *reinterpret_cast<uint4*>(to[x] + 32 * e) = v;
+          for (int y = 0; y < 8; ++y) {
+            const int rr = 4 * y + (lane >> 3);
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+            if (to[y] >= 0) *reinterpret_cast<uint4*>(out + to[y] + 64 * e) = v;
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
       fence_before();  // O is read before the next item's first product is let go
     }

@@ -400,6 +400,16 @@ def test_prompt_several_items_a_block(kvs, G, H, window, sinks):
     _prompt(kvs, [1500, 1700, 3, 700], [1500, 900, 3, 640], G, H, 32, window, sinks, seed=G)
 
 
+@pytest.mark.parametrize("R,G,H,most,window,sinks", [(100, 3, 4, 60, 0, 0), (170, 2, 8, 40, 33, 3), (31, 8, 5, 200, 0, 0)])
+def test_prompt_items_of_many_requests(kvs, R, G, H, most, window, sinks):
+    """Items of many short requests, some without a new token, several a block: found from request to request."""
+    rng = np.random.default_rng(R)
+    new = [int(x) * (i % 5 != 2) for i, x in enumerate(rng.integers(0, most, R))]
+    lens = [c + int(x) for c, x in zip(new, rng.integers(0, 300, R))]
+    new[40:60] = [0] * len(new[40:60])  # and a run of them
+    _prompt(kvs, lens, new, G, H, 16, window, sinks, seed=R)
+
+
 @pytest.mark.parametrize("H", [1, 4, 5, 8])
 @pytest.mark.parametrize("lens,new,G,page,window,sinks", [
     ([9000], [3], 1, 64, 0, 0), ([9000, 100, 0, 5000], [5, 100, 0, 1], 2, 16, 0, 0),
