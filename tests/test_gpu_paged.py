@@ -215,6 +215,27 @@ def test_decode_many_short_rows(kvs, R, G, H, window, sinks):
     ref.check_decode(out, lse, q, k, v, table, lens, window, sinks, SC)
 
 
+@pytest.mark.parametrize("R,G,H,window,sinks", [(400, 2, 4, 0, 0), (700, 1, 7, 40, 9), (90, 8, 2, 0, 0), (700, 1, 8, 300, 0)])
+def test_decode_many_rows_with_weights(kvs, R, G, H, window, sinks):
+    """Rows joined and weighed by kernels of their own: empty, short and long ones (over more than one piece)."""
+    rng = np.random.default_rng(R + H)
+    lens = [int(x) for x in rng.integers(1, 200, R)]
+    for i in range(0, R, 4):
+        lens[i] = 0
+    lens[1], lens[R // 2] = 3001, 1024
+    k, v, table, n = ref.make(lens, G, 16, seed=R, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(R, G, H, D, device=DEV)
+    before = torch.rand(R, G, cache.cap, device=DEV)
+    mass = before.clone()
+    out, lse = kvs.paged_decode_attn(q, cache, window, sinks, mass=mass)
+    ref.check_decode(out, lse, q, k, v, table, lens, window, sinks, SC, before, mass)
+    for r in range(R):
+        hidden = torch.ones(cache.cap, dtype=torch.bool, device=DEV)
+        hidden[torch.from_numpy(ref.visible(lens[r] - 1, window, sinks)).to(DEV)] = False
+        assert torch.equal(mass[r][:, hidden], before[r][:, hidden])
+
+
 @pytest.mark.parametrize("R", [1, 200, 600])
 def test_decode_nothing_seen(kvs, R):
     k, v, table, n = ref.make([0] * R, 2, 16, seed=R, poison=False)
