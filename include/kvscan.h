@@ -512,6 +512,16 @@ KVS_API kvs_status paged_decode_attn(const kvs_paged_decode_args* a, void* ws, s
                                      int32_t* dev_status, void* stream);
 KVS_API size_t kvs_paged_decode_workspace_size(int32_t R, int32_t G, int32_t H, int32_t weight_cap);
 
+/* kvs_selftest_paged_decode_timeout -- kvs_selftest_scan_timeout's check for
+ * paged_decode_attn (bf16 queries, no weights): in every block with two units
+ * of 64 tokens or more to do, warp `warp` stops at the second as though its
+ * wait had run out, 0..3 one that computes while the other three go on, 4 the
+ * one that loads; every wait is bounded by wait_cycles. KVS_ETIMEOUT reaches
+ * dev_status (required here) and the call ends, out and lse not meaningful. */
+KVS_API kvs_status kvs_selftest_paged_decode_timeout(const kvs_paged_decode_args* a, void* ws, size_t ws_bytes,
+                                                     int32_t warp, int64_t wait_cycles, int32_t* dev_status,
+                                                     void* stream);
+
 /* paged_prompt_attn -- causal attention of the newest tokens of each request,
  * a prompt or a chunk of one, over its cached tokens (their own rows are
  * already in the cache). With c = cu[r+1] - cu[r] queries (cu device int32

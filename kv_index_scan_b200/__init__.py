@@ -128,6 +128,8 @@ def _declare():
     L.paged_decode_attn.restype = I32
     L.kvs_paged_decode_workspace_size.argtypes = [I32, I32, I32, I32]
     L.kvs_paged_decode_workspace_size.restype = SZ
+    L.kvs_selftest_paged_decode_timeout.argtypes = [ctypes.POINTER(PagedDecodeArgsC), P, SZ, I32, I64, P, P]
+    L.kvs_selftest_paged_decode_timeout.restype = I32
     L.paged_prompt_attn.argtypes = [ctypes.POINTER(PagedPromptArgsC), P, SZ, P, P]
     L.paged_prompt_attn.restype = I32
     L.kvs_paged_prompt_workspace_size.argtypes = [I32] * 7
@@ -719,6 +721,22 @@ def paged_decode_attn(q: torch.Tensor, cache: PagedKV, window: int = 0, sinks: i
     _check(_lib.paged_decode_attn(ctypes.byref(a), ws.data_ptr(), ws.numel(), _ptr(dev_status), _raw_stream(dev)),
            "paged_decode_attn")
     return out, lse
+
+
+def selftest_paged_decode_timeout(q: torch.Tensor, cache: PagedKV, warp: int, wait_cycles: int,
+                                  dev_status: torch.Tensor, stream=None):
+    """kvs_selftest_paged_decode_timeout: paged_decode_attn of bf16 queries with one warp of every block giving
+    up a wait; dev_status (device int32) receives KVS_ETIMEOUT. For tests of the failure path."""
+    dev = cache.device
+    with _on(dev, stream):
+        H = q.shape[2]
+        _need("q", q, (cache.R, cache.G, H, cache.D), torch.bfloat16, dev)
+        out = torch.empty(q.shape, dtype=torch.float32, device=dev)
+        ws = paged_decode_workspace(cache, H)
+        a = PagedDecodeArgsC(cache._ref, q.data_ptr(), KVS_BF16, H, 0, 0, 1.0, out.data_ptr(), None, None, None)
+        _check(_lib.kvs_selftest_paged_decode_timeout(ctypes.byref(a), ws.data_ptr(), ws.numel(), warp, wait_cycles,
+                                                      _ptr(dev_status), _raw_stream(dev)),
+               "kvs_selftest_paged_decode_timeout")
 
 
 def paged_prompt_attn(q: torch.Tensor, cu: torch.Tensor, cache: PagedKV, window: int = 0, sinks: int = 0,

@@ -34,12 +34,13 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-// Waits for the phase of this parity; false if it does not come.
-__device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity) {
+// Waits for the phase of this parity; false if it does not come. (A thread that
+// was held up between its last try and the clock looks once more.)
+__device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, long long cycles = kWaitCycles) {
   if (mbar_try(b, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try(b, parity))
-    if (clock64() - t0 > kWaitCycles) return false;
+    if (clock64() - t0 > cycles) return mbar_try(b, parity);
   return true;
 }
 // The page pool as a tensor [page id][head][half][token][64 elements]: `rows`

@@ -65,7 +65,9 @@ kvs_status paged_append_launch(const PagedView& kv, const uint16_t* Knew, const 
                                const int32_t* cu, int T, float* mass, int32_t* pos, const int32_t* seen,
                                int32_t* dev_status, cudaStream_t s);
 size_t paged_decode_ws_bytes(int R, int G, int H, int weight_cap);
-kvs_status paged_decode_launch(const kvs_paged_decode_args* a, void* ws, int32_t* dev_status, cudaStream_t s);
+// test_warp >= 0: that warp gives up, and waits are bounded by wait_cycles (kvs_selftest_paged_decode_timeout)
+kvs_status paged_decode_launch(const kvs_paged_decode_args* a, void* ws, int32_t* dev_status, cudaStream_t s,
+                               int test_warp = -1, int64_t wait_cycles = 0);
 size_t paged_prompt_ws_bytes(int R, int G, int H, int T, int cap, int window, int sinks);
 kvs_status paged_prompt_launch(const kvs_paged_prompt_args* a, void* ws, int32_t* dev_status, cudaStream_t s);
 size_t paged_evict_ws_bytes(int R, int G, int budget);

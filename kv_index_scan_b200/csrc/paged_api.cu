@@ -61,6 +61,24 @@ kvs_status check_mask(const char* who, int window, int sinks, float scale) {
   return KVS_OK;
 }
 
+kvs_status check_decode(const kvs_paged_decode_args* a, const void* ws, size_t ws_bytes) {
+  KVS_REQUIRE(a != nullptr, KVS_EINVAL, "paged_decode_attn: args is null");
+  KVS_PROPAGATE(check_paged("paged_decode_attn", a->kv));
+  KVS_PROPAGATE(check_mask("paged_decode_attn", a->window, a->sinks, a->scale));
+  KVS_REQUIRE(a->q && a->out, KVS_EINVAL, "paged_decode_attn: q and out must be non-null");
+  KVS_REQUIRE(a->q_dtype == KVS_F32 || a->q_dtype == KVS_BF16, KVS_EINVAL, "paged_decode_attn: q_dtype=%d", a->q_dtype);
+  KVS_REQUIRE(a->H >= 1 && a->H <= 8, KVS_EINVAL, "paged_decode_attn: H=%d query heads per KV head (1..8)", a->H);
+  KVS_REQUIRE(aligned16(a->q) && aligned16(a->out), KVS_EINVAL, "paged_decode_attn: q and out must be 16-byte aligned");
+  KVS_REQUIRE((a->mass == nullptr) == (a->mass_out == nullptr), KVS_EINVAL,
+              "paged_decode_attn: mass and mass_out go together");
+  const size_t need =
+      paged_decode_ws_bytes(a->kv->R, a->kv->G, a->H, a->mass ? a->kv->max_pages * a->kv->page : 0);
+  KVS_REQUIRE(need == 0 || (ws && ws_bytes >= need), KVS_EWORKSPACE, "paged_decode_attn: workspace %zu < %zu bytes",
+              ws_bytes, need);
+  KVS_REQUIRE(aligned16(ws), KVS_EINVAL, "paged_decode_attn: the workspace must be 16-byte aligned");
+  return KVS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -89,21 +107,20 @@ size_t kvs_paged_decode_workspace_size(int32_t R, int32_t G, int32_t H, int32_t 
 
 kvs_status paged_decode_attn(const kvs_paged_decode_args* a, void* ws, size_t ws_bytes, int32_t* dev_status,
                              void* stream) {
-  KVS_REQUIRE(a != nullptr, KVS_EINVAL, "paged_decode_attn: args is null");
-  KVS_PROPAGATE(check_paged("paged_decode_attn", a->kv));
-  KVS_PROPAGATE(check_mask("paged_decode_attn", a->window, a->sinks, a->scale));
-  KVS_REQUIRE(a->q && a->out, KVS_EINVAL, "paged_decode_attn: q and out must be non-null");
-  KVS_REQUIRE(a->q_dtype == KVS_F32 || a->q_dtype == KVS_BF16, KVS_EINVAL, "paged_decode_attn: q_dtype=%d", a->q_dtype);
-  KVS_REQUIRE(a->H >= 1 && a->H <= 8, KVS_EINVAL, "paged_decode_attn: H=%d query heads per KV head (1..8)", a->H);
-  KVS_REQUIRE(aligned16(a->q) && aligned16(a->out), KVS_EINVAL, "paged_decode_attn: q and out must be 16-byte aligned");
-  KVS_REQUIRE((a->mass == nullptr) == (a->mass_out == nullptr), KVS_EINVAL,
-              "paged_decode_attn: mass and mass_out go together");
-  const size_t need =
-      paged_decode_ws_bytes(a->kv->R, a->kv->G, a->H, a->mass ? a->kv->max_pages * a->kv->page : 0);
-  KVS_REQUIRE(need == 0 || (ws && ws_bytes >= need), KVS_EWORKSPACE, "paged_decode_attn: workspace %zu < %zu bytes",
-              ws_bytes, need);
-  KVS_REQUIRE(aligned16(ws), KVS_EINVAL, "paged_decode_attn: the workspace must be 16-byte aligned");
+  KVS_PROPAGATE(check_decode(a, ws, ws_bytes));
   KVS_PROPAGATE(paged_decode_launch(a, ws, dev_status, static_cast<cudaStream_t>(stream)));
+  return ok();
+}
+
+kvs_status kvs_selftest_paged_decode_timeout(const kvs_paged_decode_args* a, void* ws, size_t ws_bytes, int32_t warp,
+                                             int64_t wait_cycles, int32_t* dev_status, void* stream) {
+  KVS_PROPAGATE(check_decode(a, ws, ws_bytes));
+  KVS_REQUIRE(dev_status && warp >= 0 && warp <= 4 && wait_cycles >= 1000 && wait_cycles <= 2000000000LL, KVS_EINVAL,
+              "kvs_selftest_paged_decode_timeout: dev_status is required, warp=%d (0..4), wait_cycles=%lld (1e3 .. 2e9)",
+              warp, static_cast<long long>(wait_cycles));
+  KVS_REQUIRE(a->q_dtype == KVS_BF16 && !a->mass, KVS_EUNSUPPORTED,
+              "kvs_selftest_paged_decode_timeout: bf16 queries without weights");
+  KVS_PROPAGATE(paged_decode_launch(a, ws, dev_status, static_cast<cudaStream_t>(stream), warp, wait_cycles));
   return ok();
 }
 

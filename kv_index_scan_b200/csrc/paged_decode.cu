@@ -48,6 +48,7 @@ constexpr int kBlocksPerSM = 2;
 constexpr int kPoolBytes = kUnit * kD * 2;     // K or V of a unit
 constexpr int kStageBytes = 2 * kPoolBytes;
 constexpr int kMinUnits = 2;                   // units a block takes at least
+constexpr int kTestUnit = 1;
 constexpr int kPartRow = kD + 4;               // maximum, sum, -, -, output
 constexpr int kPartSlots = 2;
 
@@ -67,6 +68,7 @@ struct DecodeSmem {
   float ml[kConsumers - 1][8][2];
   UnitInfo info[kStages];
   uint64_t full[kStages], empty[kStages];
+  uint64_t parts_in, parts_out;  // the merge of a row: parts of the other warps there, and taken by warp 0
   int abort_flag;
 };
 
@@ -85,6 +87,8 @@ struct DecodeParams {
   int hp;          // H rounded up to 2, 4 or 8
   int blocks;
   int32_t* dev_status;
+  long long wait_cycles;  // of the self-test
+  int test_warp;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -151,7 +155,9 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t&
   return before + inc - v;
 }
 
-template <bool kF32Q, bool kWeights>
+// kTest: every wait is bounded by wait_cycles, and in every block that has as many
+// units warp test_warp gives up at unit kTestUnit.
+template <bool kF32Q, bool kWeights, bool kTest = false>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(const DecodeParams p,
                                                                               const __grid_constant__ CUtensorMap mapK,
                                                                               const __grid_constant__ CUtensorMap mapV) {
@@ -167,6 +173,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], kConsumers);
     }
+    mbar_init(&sm.parts_in, kConsumers - 1);
+    mbar_init(&sm.parts_out, 1);
     sm.abort_flag = 0;
     mbar_init_fence();
     tma_prefetch_map(&mapK);
@@ -208,11 +216,21 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
   __syncthreads();
   const int units = static_cast<int>(u1 - u0);
 
-  auto fail = [&] {
-    set_status(p.dev_status, KVS_ETIMEOUT);
-    atomicExch(&sm.abort_flag, 1);
-  };
   auto aborted = [&] { return *reinterpret_cast<volatile int*>(&sm.abort_flag) != 0; };
+  // By a whole warp, every lane for itself (what the barrier guards is ordered for
+  // the lanes that have seen its phase). A warp whose wait runs out leaves, and the
+  // others, which may have seen the same phase come, run out of their own next
+  // waits: no warp meets another at anything but such a wait.
+  const long long limit = kTest ? p.wait_cycles : kWaitCycles;
+  auto wait = [&](uint64_t* b, uint32_t parity) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try(b, parity))) return true;
+    if (__all_sync(0xFFFFFFFFu, !aborted() && mbar_wait(b, parity, limit))) return true;
+    if (lane == 0) {
+      set_status(p.dev_status, KVS_ETIMEOUT);
+      atomicExch(&sm.abort_flag, 1);
+    }
+    return false;
+  };
 
   if (warp == kConsumers) {
     // ---------------- loads ----------------
@@ -261,16 +279,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
         look(i + 1);
       }
       const unsigned have = __ballot_sync(0xFFFFFFFFu, id >= 0);
-      int ok = 1;
-      if (lane == 0) {
-        if (i >= kStages && !mbar_wait(&sm.empty[st], (i / kStages - 1) & 1)) {
-          fail();
-          ok = 0;
-        }
-        if (aborted()) ok = 0;
-      }
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-      if (!ok) break;
+      if (i >= kStages && !wait(&sm.empty[st], (i / kStages - 1) & 1)) break;
+      if (kTest && p.test_warp == kConsumers && i == kTestUnit) break;  // (this unit never comes)
       if (lane == 0) {
         int groups = 0;  // 16-token groups that are there
         for (int e = 0; e < 4; ++e)
@@ -289,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
     }
     // no copy may be in flight when the block ends
     if (lane == 0)
-      for (int i = max(0, issued - kStages); i < issued; ++i) mbar_wait(&sm.full[i % kStages], (i / kStages) & 1);
+      for (int i = max(0, issued - kStages); i < issued; ++i) mbar_wait(&sm.full[i % kStages], (i / kStages) & 1, limit);
     return;
   }
 
@@ -327,16 +337,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
       }
   };
   load_q(s_r * G + s_g);  // while the first unit is on its way
+  uint32_t merged = 0;    // rows, or parts of rows, that have ended here
   for (int i = 0; i < units; ++i) {
     const int st = i % kStages;
-    int ok = 1;
-    if (lane == 0 && !mbar_wait(&sm.full[st], (i / kStages) & 1)) {
-      fail();
-      ok = 0;
-    }
-    // a stage that one warp has seen full stays so until all have released it:
-    // the four warps stop at the same unit, and none is left at a barrier
-    if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+    if (!wait(&sm.full[st], (i / kStages) & 1)) break;
+    if (kTest && p.test_warp == warp && i == kTestUnit) break;  // (as though the wait had run out)
     const UnitInfo info = sm.info[st];
     if (info.flags & kFirst) {
       // a new row
@@ -443,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
         lB += __shfl_xor_sync(0xFFFFFFFFu, lB, d);
       }
       if (warp > 0) {
+        if (merged > 0 && !wait(&sm.parts_out, (merged - 1) & 1)) break;
         float(&mo)[8][kD] = sm.merge[warp - 1];
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
@@ -457,9 +463,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
           sm.ml[warp - 1][hB][0] = mB;
           sm.ml[warp - 1][hB][1] = lB;
         }
-      }
-      asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kConsumers) : "memory");
-      if (warp == 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.parts_in);
+      } else {
+        if (!wait(&sm.parts_in, merged & 1)) break;
         float MA = mA, MB = mB;
 #pragma unroll
         for (int w = 0; w < kConsumers - 1; ++w) {
@@ -491,6 +498,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
             o[mt][3] = fmaf(mo[hB][16 * mt + gq + 8], cB, o[mt][3]);
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.parts_out);
         const int slot = info.flags >> kSlotShift;
         float *dA, *dB;
         float iA = 1.f, iB = 1.f;
@@ -526,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
           }
         }
       }
-      asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kConsumers) : "memory");
+      ++merged;
     }
   }
 }
@@ -872,15 +881,15 @@ size_t carve(DecodeParams* p, void* ws, int R, int G, int H, int weight_cap) {
   return align_up(c.used, 16);
 }
 
-template <bool kF32Q, bool kWeights>
+template <bool kF32Q, bool kWeights, bool kTest = false>
 kvs_status launch(const DecodeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
   const int64_t cap = static_cast<int64_t>(p.kv.max_pages) << p.kv.shift;
   const int64_t chunks = kWeights ? (cap + kJoinTokens - 1) / kJoinTokens : 1, joins = chunks * p.kv.R * p.kv.G;
   KVS_REQUIRE(joins < (1ll << 31), KVS_EUNSUPPORTED, "paged_decode_attn: weights of R*G=%d rows of %lld tokens",
               p.kv.R * p.kv.G, static_cast<long long>(cap));
-  allow_smem<paged_decode_kernel<kF32Q, kWeights>>(sizeof(DecodeSmem));
-  launch_chained(paged_decode_kernel<kF32Q, kWeights>, dim3(p.blocks), dim3(kThreads), sizeof(DecodeSmem), s, p, mk,
-                 mv);
+  allow_smem<paged_decode_kernel<kF32Q, kWeights, kTest>>(sizeof(DecodeSmem));
+  launch_chained(paged_decode_kernel<kF32Q, kWeights, kTest>, dim3(p.blocks), dim3(kThreads), sizeof(DecodeSmem), s, p,
+                 mk, mv);
   const int rows = p.kv.R * p.kv.G;
   if (rows <= (kWeights ? kWeighRowsPerSM : 1) * sm_count()) {
     const dim3 grid(static_cast<unsigned>(joins));
@@ -905,7 +914,8 @@ kvs_status launch(const DecodeParams& p, const CUtensorMap& mk, const CUtensorMa
 
 size_t paged_decode_ws_bytes(int R, int G, int H, int weight_cap) { return carve(nullptr, nullptr, R, G, H, weight_cap); }
 
-kvs_status paged_decode_launch(const kvs_paged_decode_args* a, void* ws, int32_t* dev_status, cudaStream_t s) {
+kvs_status paged_decode_launch(const kvs_paged_decode_args* a, void* ws, int32_t* dev_status, cudaStream_t s,
+                               int test_warp, int64_t wait_cycles) {
   DecodeParams p{};
   p.kv = paged_view(a->kv);
   p.q = a->q;
@@ -924,6 +934,9 @@ kvs_status paged_decode_launch(const kvs_paged_decode_args* a, void* ws, int32_t
   CUtensorMap mk, mv;
   KVS_PROPAGATE(paged_tensor_map(&mk, a->kv->K, p.kv, rows, 2, "paged_decode_attn"));
   KVS_PROPAGATE(paged_tensor_map(&mv, a->kv->V, p.kv, rows, 2, "paged_decode_attn"));
+  p.test_warp = test_warp;
+  p.wait_cycles = wait_cycles;
+  if (test_warp >= 0) return launch<false, false, true>(p, mk, mv, s);
   const bool f32 = a->q_dtype == KVS_F32;
   if (f32) return a->mass ? launch<true, true>(p, mk, mv, s) : launch<true, false>(p, mk, mv, s);
   return a->mass ? launch<false, true>(p, mk, mv, s) : launch<false, false>(p, mk, mv, s);

@@ -343,6 +343,28 @@ def test_decode_caller_buffers_streams_and_graph(kvs):
         ref.check_decode(out, lse, q, k, v, table, m, 200, 2, SC)
 
 
+@pytest.mark.parametrize("warp", [0, 1, 2, 3, 4])
+@pytest.mark.parametrize("lens", [[20000, 7, 9000], [100] * 300])
+def test_decode_bounded_waits_run_out_and_the_call_ends(kvs, lens, warp):
+    """One warp of every block stops at its second unit as though its wait had run out, while the others have
+    seen the same phase come: they end too, the status word says so, and the next call is right. Rows longer
+    than a block's run, and rows that end in the middle of it, where the four warps meet."""
+    import time
+    k, v, table, n = ref.make(lens, 2, 64, seed=51, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(len(lens), 2, 4, D, device=DEV).to(torch.bfloat16)
+    st = _status()
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    kvs.selftest_paged_decode_timeout(q, cache, warp, 2_000_000, st)
+    torch.cuda.synchronize()
+    assert int(st) == kvs.KVS_ETIMEOUT and time.perf_counter() - t0 < 5.0
+    st = _status()
+    out, lse = kvs.paged_decode_attn(q, cache, dev_status=st)
+    ref.check_decode(out, lse, q, k, v, table, lens, 0, 0, SC)
+    assert int(st) == 0
+
+
 def test_binding_refusals(kvs):
     k, v, table, n = ref.make([20], 2, 16, seed=1)
     cache = kvs.PagedKV(k, v, table, n)

@@ -133,3 +133,18 @@ def test_binding_refuses_host_tensors(kvs):
         kvs.PagedKV(pool, pool, torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError, match="k_pages"):
         kvs.PagedKV(pool.float(), pool, torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+def test_decode_timeout_selftest_checks(kvs):
+    """The failure-path self-test refuses bad arguments before any launch."""
+    kv = _kv(kvs)
+    f = dict(kv=ctypes.pointer(kv), q=4096, q_dtype=1, H=4, window=0, sinks=0, scale=1.0, out=4096, lse=None,
+             mass=None, mass_out=None)
+    def call(warp=0, cycles=10 ** 6, status=4096, ws=1 << 40, **change):
+        a = kvs.PagedDecodeArgsC(*{**f, **change}.values())
+        return kvs._lib.kvs_selftest_paged_decode_timeout(ctypes.byref(a), 4096, ws, warp, cycles, status, None)
+    for bad in (dict(warp=-1), dict(warp=5), dict(cycles=999), dict(cycles=3 * 10 ** 9), dict(status=None), dict(q=None),
+                dict(H=9)):
+        assert call(**bad) == kvs.KVS_EINVAL, bad
+    assert call(q_dtype=0) == kvs.KVS_EUNSUPPORTED and call(mass=4096, mass_out=4096) == kvs.KVS_EUNSUPPORTED
+    assert call(ws=0) == kvs.KVS_EWORKSPACE
