@@ -559,6 +559,13 @@ KVS_API kvs_status paged_prompt_attn(const kvs_paged_prompt_args* a, void* ws, s
 KVS_API size_t kvs_paged_prompt_workspace_size(int32_t R, int32_t G, int32_t H, int32_t T, int32_t cap,
                                                int32_t window, int32_t sinks);
 
+/* kvs_selftest_paged_prompt_timeout -- the same check for paged_prompt_attn
+ * (not split): in every block with two tiles of 128 tokens or more to do, warp
+ * `warp` gives up at the second (0..7 one of the softmax, 8 the loads, 9 the
+ * products, 10 and 11 those that clear rows of V). */
+KVS_API kvs_status kvs_selftest_paged_prompt_timeout(const kvs_paged_prompt_args* a, int32_t warp,
+                                                     int64_t wait_cycles, int32_t* dev_status, void* stream);
+
 /* kvs_paged_evict -- cuts every request that holds more than `budget` tokens
  * down to `budget`, for each KV head by itself. Of the n[r] slots it keeps
  * first those whose token's place pos is < sinks or >= seen[r] - recent (the

@@ -134,6 +134,8 @@ def _declare():
     L.paged_prompt_attn.restype = I32
     L.kvs_paged_prompt_workspace_size.argtypes = [I32] * 7
     L.kvs_paged_prompt_workspace_size.restype = SZ
+    L.kvs_selftest_paged_prompt_timeout.argtypes = [ctypes.POINTER(PagedPromptArgsC), I32, I64, P, P]
+    L.kvs_selftest_paged_prompt_timeout.restype = I32
     L.kvs_paged_evict.argtypes = [ctypes.POINTER(PagedEvictArgsC), P, SZ, P, P]
     L.kvs_paged_evict.restype = I32
     L.kvs_paged_evict_workspace_size.argtypes = [I32, I32, I32]
@@ -782,6 +784,23 @@ def paged_prompt_attn(q: torch.Tensor, cu: torch.Tensor, cache: PagedKV, window:
         wp, wn = ws.data_ptr(), ws.numel()
     _check(_lib.paged_prompt_attn(ctypes.byref(a), wp, wn, _ptr(dev_status), _raw_stream(dev)), "paged_prompt_attn")
     return out, lse
+
+
+def selftest_paged_prompt_timeout(q: torch.Tensor, cu: torch.Tensor, cache: PagedKV, warp: int, wait_cycles: int,
+                                  dev_status: torch.Tensor, stream=None):
+    """kvs_selftest_paged_prompt_timeout: paged_prompt_attn with one warp of every block giving up; dev_status
+    (device int32) receives KVS_ETIMEOUT. For tests of the failure path."""
+    dev = cache.device
+    with _on(dev, stream):
+        T, Hq, D = q.shape
+        _need("q", q, (T, Hq, cache.D), torch.bfloat16, dev)
+        _need("cu", cu, cache._cu_shape, torch.int32, dev)
+        _require(Hq % cache.G == 0, f"q must have a multiple of {cache.G} heads")
+        out = torch.empty_like(q)
+        a = PagedPromptArgsC(cache._ref, q.data_ptr(), Hq * D, cu.data_ptr(), T, Hq // cache.G, 0, 0, 1.0,
+                             out.data_ptr(), Hq * D, None)
+        _check(_lib.kvs_selftest_paged_prompt_timeout(ctypes.byref(a), warp, wait_cycles, _ptr(dev_status),
+                                                      _raw_stream(dev)), "kvs_selftest_paged_prompt_timeout")
 
 
 def paged_evict(cache: PagedKV, mass: torch.Tensor, budget: int, sinks: int = 0, recent: int = 0, pos=None,

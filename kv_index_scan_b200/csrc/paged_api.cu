@@ -79,6 +79,24 @@ kvs_status check_decode(const kvs_paged_decode_args* a, const void* ws, size_t w
   return KVS_OK;
 }
 
+kvs_status check_prompt(const kvs_paged_prompt_args* a) {
+  KVS_REQUIRE(a != nullptr, KVS_EINVAL, "paged_prompt_attn: args is null");
+  KVS_PROPAGATE(check_paged("paged_prompt_attn", a->kv));
+  KVS_PROPAGATE(check_mask("paged_prompt_attn", a->window, a->sinks, a->scale));
+  KVS_REQUIRE(a->T >= 0, KVS_EINVAL, "paged_prompt_attn: T=%d", a->T);
+  KVS_REQUIRE(a->H >= 1 && a->H <= 8, KVS_EINVAL, "paged_prompt_attn: H=%d query heads per KV head (1..8)", a->H);
+  if (a->T == 0) return KVS_OK;
+  KVS_REQUIRE(a->q && a->out && a->cu, KVS_EINVAL, "paged_prompt_attn: q, out and cu must be non-null");
+  const int64_t width = static_cast<int64_t>(a->kv->G) * a->H * kD;
+  KVS_REQUIRE(a->q_ld >= width && a->q_ld % 8 == 0 && a->out_ld >= width && a->out_ld % 8 == 0, KVS_EINVAL,
+              "paged_prompt_attn: q_ld=%lld out_ld=%lld must be multiples of 8, at least G*H*128",
+              static_cast<long long>(a->q_ld), static_cast<long long>(a->out_ld));
+  KVS_REQUIRE(static_cast<int64_t>(a->T) * a->H < (1ll << 31) - 4096, KVS_EUNSUPPORTED,
+              "paged_prompt_attn: T*H=%lld rows (below 2^31)", static_cast<long long>(a->T) * a->H);
+  KVS_REQUIRE(aligned16(a->q) && aligned16(a->out), KVS_EINVAL, "paged_prompt_attn: q and out must be 16-byte aligned");
+  return KVS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -131,26 +149,26 @@ size_t kvs_paged_prompt_workspace_size(int32_t R, int32_t G, int32_t H, int32_t 
 
 kvs_status paged_prompt_attn(const kvs_paged_prompt_args* a, void* ws, size_t ws_bytes, int32_t* dev_status,
                              void* stream) {
-  KVS_REQUIRE(a != nullptr, KVS_EINVAL, "paged_prompt_attn: args is null");
-  KVS_PROPAGATE(check_paged("paged_prompt_attn", a->kv));
-  KVS_PROPAGATE(check_mask("paged_prompt_attn", a->window, a->sinks, a->scale));
-  KVS_REQUIRE(a->T >= 0, KVS_EINVAL, "paged_prompt_attn: T=%d", a->T);
-  KVS_REQUIRE(a->H >= 1 && a->H <= 8, KVS_EINVAL, "paged_prompt_attn: H=%d query heads per KV head (1..8)", a->H);
+  KVS_PROPAGATE(check_prompt(a));
   if (a->T == 0) return ok();
-  KVS_REQUIRE(a->q && a->out && a->cu, KVS_EINVAL, "paged_prompt_attn: q, out and cu must be non-null");
-  const int64_t width = static_cast<int64_t>(a->kv->G) * a->H * kD;
-  KVS_REQUIRE(a->q_ld >= width && a->q_ld % 8 == 0 && a->out_ld >= width && a->out_ld % 8 == 0, KVS_EINVAL,
-              "paged_prompt_attn: q_ld=%lld out_ld=%lld must be multiples of 8, at least G*H*128",
-              static_cast<long long>(a->q_ld), static_cast<long long>(a->out_ld));
-  KVS_REQUIRE(static_cast<int64_t>(a->T) * a->H < (1ll << 31) - 4096, KVS_EUNSUPPORTED,
-              "paged_prompt_attn: T*H=%lld rows (below 2^31)", static_cast<long long>(a->T) * a->H);
-  KVS_REQUIRE(aligned16(a->q) && aligned16(a->out), KVS_EINVAL, "paged_prompt_attn: q and out must be 16-byte aligned");
   const size_t need = paged_prompt_ws_bytes(a->kv->R, a->kv->G, a->H, a->T, a->kv->max_pages * a->kv->page, a->window,
                                            a->sinks);
   KVS_REQUIRE(need == 0 || (ws && ws_bytes >= need), KVS_EWORKSPACE, "paged_prompt_attn: workspace %zu < %zu bytes",
               ws_bytes, need);
   KVS_REQUIRE(aligned16(ws), KVS_EINVAL, "paged_prompt_attn: the workspace must be 16-byte aligned");
   KVS_PROPAGATE(paged_prompt_launch(a, ws, dev_status, static_cast<cudaStream_t>(stream)));
+  return ok();
+}
+
+kvs_status kvs_selftest_paged_prompt_timeout(const kvs_paged_prompt_args* a, int32_t warp, int64_t wait_cycles,
+                                             int32_t* dev_status, void* stream) {
+  KVS_PROPAGATE(check_prompt(a));
+  KVS_REQUIRE(a->T > 0 && dev_status && warp >= 0 && warp <= 11 && wait_cycles >= 1000 && wait_cycles <= 2000000000LL,
+              KVS_EINVAL,
+              "kvs_selftest_paged_prompt_timeout: queries and dev_status are required, warp=%d (0..11), wait_cycles=%lld "
+              "(1e3 .. 2e9)",
+              warp, static_cast<long long>(wait_cycles));
+  KVS_PROPAGATE(paged_prompt_launch(a, nullptr, dev_status, static_cast<cudaStream_t>(stream), warp, wait_cycles));
   return ok();
 }
 

@@ -65,6 +65,7 @@ constexpr int kThreads = 32 * 12;             // three warpgroups
 constexpr int kSoftRegs = 208, kOtherRegs = 88;
 constexpr int kMaxPieces = 32;               // of an item (a lane of the join each)
 constexpr int kPieceTiles = 4;               // that a piece has at least
+constexpr int kTestTile = 1;
 constexpr float kGrow = 8.f;                 // log2 of the growth that a maximum may lag behind
 
 struct PromptSmem {
@@ -94,6 +95,8 @@ struct PromptParams {
   float* part_o;     // [pieces][T][G*H][128], relative to the row's maximum in that piece
   float2* part_ml;   // [pieces][T][G*H]: that maximum (base 2), the sum
   int32_t* dev_status;
+  long long wait_cycles;  // of the self-test
+  int test_warp;
 
   // the first packed row of request r, within the T there are
   __device__ __forceinline__ int start(int r) const {
@@ -307,7 +310,9 @@ __device__ __forceinline__ bool find_item(const PromptParams& p, uint32_t x, int
   return false;
 }
 
-template <bool kPieces>
+// kTest: every wait is bounded by wait_cycles, and in every block that has as many
+// tiles warp test_warp gives up at tile kTestTile.
+template <bool kPieces, bool kTest = false>
 __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptParams p,
                                                                    const __grid_constant__ CUtensorMap mapQ,
                                                                    const __grid_constant__ CUtensorMap mapK,
@@ -377,13 +382,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
     atomicExch(&sm.abort_flag, 1);
   };
   auto aborted = [&] { return *reinterpret_cast<volatile int*>(&sm.abort_flag) != 0; };
+  // By the whole warp, every lane for itself (what the barrier guards is ordered for
+  // the lanes that have seen its phase), and first without looking whether the block
+  // has given up: the products' warp waits seven times a tile, and mostly for what is
+  // there.
+  const long long limit = kTest ? p.wait_cycles : kWaitCycles;
   auto wait = [&](uint64_t* b, uint32_t parity) {
-    if (!aborted() && mbar_wait(b, parity)) return true;
+    if (!aborted() && mbar_wait(b, parity, limit)) return true;
     fail();
     return false;
   };
-  // by the whole warp (first without looking whether the block has given up:
-  // the products' warp waits seven times a tile, and mostly for what is there)
   auto wait_all = [&](uint64_t* b, uint32_t parity) {
     if (__all_sync(0xFFFFFFFFu, mbar_try(b, parity))) return true;
     return __all_sync(0xFFFFFFFFu, wait(b, parity)) != 0;
@@ -424,21 +432,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
         const int slot = round % kItems;
         Item<kPieces> then;
         const bool is = find(then);
-        int go = 1;
+        if (round >= kItems && !wait_all(&sm.item_empty[slot], (round / kItems - 1) & 1)) return false;
         if (lane == 0) {
-          if (round >= kItems) go = wait(&sm.item_empty[slot], (round / kItems - 1) & 1);
-          if (go) {
-            int4 w[4] = {};
-            memcpy(w, &then, sizeof(then));
-            w[3].w = is;
+          int4 w[4] = {};
+          memcpy(w, &then, sizeof(then));
+          w[3].w = is;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) sm.items[slot][x] = w[x];
-            mbar_arrive(&sm.item_full[slot]);
-          }
+          for (int x = 0; x < 4; ++x) sm.items[slot][x] = w[x];
+          mbar_arrive(&sm.item_full[slot]);
         }
         ++round;
         __syncwarp();
-        return __shfl_sync(0xFFFFFFFFu, go, 0) != 0;
+        return true;
       };
       ok = hand_on();
       bool more = ok && read_item(0, it);
@@ -464,39 +469,35 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
           const uint32_t to = half * kHalfBytes + sub * box * 128;
           for (int which = 0; which < 2 && ok; ++which) {
             uint64_t* full = which ? &sm.v_full[st] : &sm.k_full[st];
-            int go = 1;
-            if (lane == 0) {
-              if (at >= kStages) go = wait(which ? &sm.v_empty[st] : &sm.k_empty[st], (at / kStages - 1) & 1);
-              if (go) {
-                if (which == 0) {
-                  int there = 0;
-                  for (int e = 0; e < 8; ++e)
-                    if (have >> (2 * (16 * e / box)) & 1u) there |= 1 << e;
-                  sm.groups[at % kInfos] = there;
-                  __threadfence_block();
-                }
-                if (have) mbar_expect(full, __popc(have) * box * 128);
-                else mbar_arrive(full);
-              }
-            }
-            ok = __shfl_sync(0xFFFFFFFFu, go, 0) != 0;
+            if (at >= kStages) ok = wait_all(which ? &sm.v_empty[st] : &sm.k_empty[st], (at / kStages - 1) & 1);
+            if (kTest && p.test_warp == warp && at == kTestTile) ok = false;
             if (!ok) break;
+            if (lane == 0) {
+              if (which == 0) {
+                int there = 0;
+                for (int e = 0; e < 8; ++e)
+                  if (have >> (2 * (16 * e / box)) & 1u) there |= 1 << e;
+                sm.groups[at % kInfos] = there;
+                __threadfence_block();
+              }
+              if (have) mbar_expect(full, __popc(have) * box * 128);
+              else mbar_arrive(full);
+            }
+            __syncwarp();
             if (id >= 0)
               tma_page_rows(sm_addr(which ? sm.v[st] : sm.k[st]) + to, which ? &mapV : &mapK, in_page, half, it.g, id,
                             full);
             ++issued;
             if (i == 0 && which == 0) {  // the queries after the first K tile, whose place is free before theirs
+              if (live > 0) ok = wait_all(&sm.q_empty, (live - 1) & 1);
+              if (!ok) break;
               if (lane == 0) {
-                if (live > 0) go = wait(&sm.q_empty, (live - 1) & 1);
-                if (go) {
-                  mbar_expect(&sm.q_full, 4 * p.per * H * 128);
-                  for (int x = 0; x < 4; ++x)
-                    tma_query_rows(sm_addr(sm.q[x >> 1]) + (x & 1) * kHalfBytes, &mapQ, it.g * H,
-                                   it.q0 + it.tok0 + (x >> 1) * p.per, x & 1, &sm.q_full);
-                }
+                mbar_expect(&sm.q_full, 4 * p.per * H * 128);
+                for (int x = 0; x < 4; ++x)
+                  tma_query_rows(sm_addr(sm.q[x >> 1]) + (x & 1) * kHalfBytes, &mapQ, it.g * H,
+                                 it.q0 + it.tok0 + (x >> 1) * p.per, x & 1, &sm.q_full);
               }
-              ok = __shfl_sync(0xFFFFFFFFu, go, 0) != 0;
-              live += ok;
+              ++live;
             }
           }
           // the next item, with two tiles on their way
@@ -506,11 +507,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
         more = ok && read_item(round - 1, it);
       }
       // no copy may be in flight when the block ends
-      if (lane == 0 && live > 0) mbar_wait(&sm.q_full, (live - 1) & 1);
+      if (lane == 0 && live > 0) mbar_wait(&sm.q_full, (live - 1) & 1, limit);
       if (lane == 0)
         for (int x = max(0, issued - 2 * kStages); x < issued; ++x) {
           const int i = x / 2;
-          mbar_wait(x & 1 ? &sm.v_full[i % kStages] : &sm.k_full[i % kStages], (i / kStages) & 1);
+          mbar_wait(x & 1 ? &sm.v_full[i % kStages] : &sm.k_full[i % kStages], (i / kStages) & 1, limit);
         }
     } else if (warp >= kCleanWarp) {
       // ---------------- rows of V that no row of the block sees ----------------
@@ -518,6 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
         for (int i = 0; i < it.tiles && ok; ++i, ++at) {
           const int st = at % kStages;
           ok = wait_all(&sm.v_full[st], (at / kStages) & 1);
+          if (kTest && p.test_warp == warp && at == kTestTile) ok = false;
           if (!ok) break;
           const int t0 = it.token(i), there = sm.groups[at % kInfos];
           if (it.ragged(t0, there, p.sinks)) {
@@ -573,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
         for (int i = 0; i < it.tiles && ok; ++i, ++at) {
           const int st = at % kStages, after = at + 1;
           ok = wait_all(&sm.v_clean[st], (at / kStages) & 1);
+          if (kTest && p.test_warp == warp && at == kTestTile) ok = false;
           for (int t = 0; t < 2 && ok; ++t) {
             const uint32_t d = tmem + 256 + 128 * t, a = tmem + 128 * t;
             const uint64_t b = dv + st * (kTileBytes >> 4);
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
       }
       if (!ok) {  // products already issued end before the block does
         commit(&sm.drain);
-        mbar_wait(&sm.drain, 0);
+        mbar_wait(&sm.drain, 0, limit);
       }
     }
   } else {
@@ -631,6 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
       float m = ninf, l = 0.f;
       for (int i = 0; i < it.tiles; ++i, ++at) {
         ok = wait_all(&sm.s_full[t], at & 1);
+        if (kTest && p.test_warp == warp && at == kTestTile) ok = false;
         if (!ok) break;
         fence_after();
         const int t0 = it.token(i), there = sm.groups[at % kInfos];
@@ -883,7 +887,8 @@ size_t paged_prompt_ws_bytes(int R, int G, int H, int T, int cap, int window, in
   return carve(nullptr, nullptr, G, H, T, pieces_of(R, G, H, T, cap, window, sinks));
 }
 
-kvs_status paged_prompt_launch(const kvs_paged_prompt_args* a, void* ws, int32_t* dev_status, cudaStream_t s) {
+kvs_status paged_prompt_launch(const kvs_paged_prompt_args* a, void* ws, int32_t* dev_status, cudaStream_t s,
+                               int test_warp, int64_t wait_cycles) {
   PromptParams p{};
   p.kv = paged_view(a->kv);
   p.cu = a->cu;
@@ -903,8 +908,11 @@ kvs_status paged_prompt_launch(const kvs_paged_prompt_args* a, void* ws, int32_t
   KVS_PROPAGATE(paged_tensor_map(&mk, a->kv->K, p.kv, box, 1, "paged_prompt_attn"));
   KVS_PROPAGATE(paged_tensor_map(&mv, a->kv->V, p.kv, box, 1, "paged_prompt_attn"));
   KVS_PROPAGATE(query_tensor_map(&mq, a, p.per));
-  p.pieces = pieces_of(p.kv.R, p.kv.G, p.H, p.T, static_cast<int64_t>(a->kv->max_pages) * a->kv->page, p.window,
-                       p.sinks);
+  p.test_warp = test_warp;
+  p.wait_cycles = wait_cycles;
+  p.pieces = test_warp >= 0 ? 1
+                            : pieces_of(p.kv.R, p.kv.G, p.H, p.T, static_cast<int64_t>(a->kv->max_pages) * a->kv->page,
+                                        p.window, p.sinks);
   carve(&p, ws, p.kv.G, p.H, p.T, p.pieces);
   const int64_t items = most_items(p.kv.R, p.kv.G, p.H, p.T) * p.pieces;
   KVS_REQUIRE(items < (1ll << 31) - (1 << 20), KVS_EUNSUPPORTED, "paged_prompt_attn: T=%d queries of G=%d KV heads", a->T,
@@ -924,8 +932,12 @@ kvs_status paged_prompt_launch(const kvs_paged_prompt_args* a, void* ws, int32_t
                    sizeof(PromptSmem), s, p, mq, mk, mv);
     return KVS_OK;
   };
-  KVS_PROPAGATE(p.pieces > 1 ? go(std::integral_constant<decltype(&paged_prompt_kernel<true>), paged_prompt_kernel<true>>())
-                             : go(std::integral_constant<decltype(&paged_prompt_kernel<false>), paged_prompt_kernel<false>>()));
+  if (test_warp >= 0)
+    KVS_PROPAGATE(go(std::integral_constant<decltype(&paged_prompt_kernel<false, true>), paged_prompt_kernel<false, true>>()));
+  else if (p.pieces > 1)
+    KVS_PROPAGATE(go(std::integral_constant<decltype(&paged_prompt_kernel<true>), paged_prompt_kernel<true>>()));
+  else
+    KVS_PROPAGATE(go(std::integral_constant<decltype(&paged_prompt_kernel<false>), paged_prompt_kernel<false>>()));
   if (p.pieces > 1) {
     const int64_t rows = static_cast<int64_t>(p.T) * p.kv.G * p.H;
     launch_chained(paged_prompt_join_kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, p);

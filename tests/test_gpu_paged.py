@@ -522,6 +522,29 @@ def test_prompt_items_that_see_nothing(kvs):
     assert bool((out[:897] == 0).all()) and bool((out[1160:] == 0).all()) and int(st) == 0
 
 
+@pytest.mark.parametrize("warp", range(12))
+@pytest.mark.parametrize("lens,new", [([3000, 40, 900], [300, 40, 7]), ([200] * 300, [200] * 300)])
+def test_prompt_bounded_waits_run_out_and_the_call_ends(kvs, lens, new, warp):
+    """One warp of every block gives up at its second tile: the other roles end too, the status word says so,
+    and the next call is right. Items of many tiles, and blocks with several items."""
+    import time
+    k, v, table, n = ref.make(lens, 2, 64, seed=52, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    cu = [0] + [int(x) for x in np.cumsum(new)]
+    cut = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    q = torch.randn(cu[-1], 8, D, device=DEV).to(torch.bfloat16)
+    st = _status()
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    kvs.selftest_paged_prompt_timeout(q, cut, cache, warp, 2_000_000, st)
+    torch.cuda.synchronize()
+    assert int(st) == kvs.KVS_ETIMEOUT and time.perf_counter() - t0 < 5.0
+    st = _status()
+    out, lse = kvs.paged_prompt_attn(q, cut, cache, dev_status=st)
+    ref.check_prompt(out, lse, q, cu, k, v, table, lens, 0, 0, SC, 2)
+    assert int(st) == 0
+
+
 def test_empty_calls(kvs):
     k, v, table, n = ref.make([20], 2, 16, seed=1)
     cache = kvs.PagedKV(k, v, table, n)

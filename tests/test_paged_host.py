@@ -148,3 +148,15 @@ def test_decode_timeout_selftest_checks(kvs):
         assert call(**bad) == kvs.KVS_EINVAL, bad
     assert call(q_dtype=0) == kvs.KVS_EUNSUPPORTED and call(mass=4096, mass_out=4096) == kvs.KVS_EUNSUPPORTED
     assert call(ws=0) == kvs.KVS_EWORKSPACE
+
+
+def test_prompt_timeout_selftest_checks(kvs):
+    kv = _kv(kvs)
+    f = dict(kv=ctypes.pointer(kv), q=4096, q_ld=1024, cu=4096, T=4, H=4, window=0, sinks=0, scale=1.0, out=4096,
+             out_ld=1024, lse=None)
+    def call(warp=0, cycles=10 ** 6, status=4096, **change):
+        a = kvs.PagedPromptArgsC(*{**f, **change}.values())
+        return kvs._lib.kvs_selftest_paged_prompt_timeout(ctypes.byref(a), warp, cycles, status, None)
+    for bad in (dict(warp=-1), dict(warp=12), dict(cycles=999), dict(cycles=3 * 10 ** 9), dict(status=None), dict(T=0),
+                dict(out=None)):
+        assert call(**bad) == kvs.KVS_EINVAL, bad
