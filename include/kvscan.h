@@ -535,10 +535,10 @@ KVS_API kvs_status kvs_selftest_paged_decode_timeout(const kvs_paged_decode_args
  *   that sees nothing (p < 0) gets out = 0 and lse = -inf. Entries of cu
  *   outside 0 .. T are clamped (KVS_EBOUNDS).
  * The softmax and all sums are f32; the weights are rounded to bf16 for the
- * product with V, and out once at the end. Queries are taken 2 * floor(128 / H)
- * tokens at a time: a cached V row that is not finite makes the outputs of the
- * queries that see it not finite, and may those of other queries taken with
- * one that does; K and V rows that none of them sees have no influence on them.
+ * product with V, and out once at the end. K and V rows that a query does not
+ * see have no influence on it, whatever they hold; a value of a V row that is not
+ * finite makes that channel of the queries that see the row not finite, a K row
+ * all of theirs.
  * Workspace: kvs_paged_prompt_workspace_size(R, G, H, T, max_pages * page, window,
  * sinks), which is 0 where there are queries enough to occupy the GPU; fewer are
  * split over the tokens they see, and the parts joined. */

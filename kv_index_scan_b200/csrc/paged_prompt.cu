@@ -28,9 +28,14 @@
 //    columns. O is rescaled in tensor memory only when a row's maximum has
 //    grown by more than 2^8 since the last time: weights up to 2^8 keep their
 //    relative precision in bf16, and the sums are f32.
-//  * Two warps clear rows of V that no row of the block sees or that were not
-//    loaded (released or bad pages, behind the last token): their weights are
-//    zero, and zero times whatever lies there must not become NaN.
+//  * Two warps clear what must not meet a weight of zero, whatever lies there:
+//    rows of V that no row of the item sees or that were not loaded (released or
+//    bad pages, behind the last token), and in tiles that some rows see more of
+//    than others the single values that are not finite. Those are noted by token,
+//    and added to the outputs of the rows that do see them at the item's end. The
+//    search for them takes 1% of a long prompt's time and 3% of short items' (64
+//    prompts of 300 tokens over 300: 199 us and 205 with it); without it a NaN
+//    reached the queries in front of its token.
 // Measured: 8192 tokens of 32 heads over 8 KV heads, causal, 0.55 TFLOP: 0.44 to
 // 0.50 ms by the clocks that the power cap leaves (1.10 to 1.25 PFLOP/s; a large
 // library product reaches 1.66 in a burst and 1.40 for seconds); 2048 tokens over
@@ -59,6 +64,8 @@ constexpr int kStages = 2;                   // of K, and of V
 constexpr int kInfos = 4;
 constexpr int kItems = 4;                    // found ahead of the warps that work on them
 constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kCleanWarps = 2;
+constexpr int kCutTiles = 6;                 // of an item: three at its rows' own tokens, three at their windows' first
+constexpr int kNotes = 4;                    // of items (the clearing warps are at most two items ahead)
 constexpr int kTakers = kSoftWarps + 1 + kCleanWarps;  // warps that take items from the loads' warp
 constexpr int kThreads = 32 * 12;             // three warpgroups
 // registers a thread: 168 at launch; 8 * 208 + 4 * 88 = 12 * 168
@@ -67,6 +74,15 @@ constexpr int kMaxPieces = 32;               // of an item (a lane of the join e
 constexpr int kPieceTiles = 4;               // that a piece has at least
 constexpr int kTestTile = 1;
 constexpr float kGrow = 8.f;                 // log2 of the growth that a maximum may lag behind
+
+// Tokens that not all rows of an item see and that have values of V that are not
+// finite, as one of the clearing warps found them in its rows of each tile (eight
+// of every sixteen, a bit each).
+struct Notes {
+  int count, r, g;
+  int tok[kCutTiles];  // the first of them
+  uint32_t rows[kCutTiles][2];
+};
 
 struct PromptSmem {
   alignas(1024) unsigned char q[2][kTileBytes];
@@ -77,6 +93,7 @@ struct PromptSmem {
   uint64_t q_full, q_empty, k_full[kStages], k_empty[kStages], v_full[kStages], v_clean[kStages], v_empty[kStages];
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t s_full[2], p_full[2][2], o_full[2], drain;  // p_full by tile and half of the tokens
+  Notes notes[kNotes][kCleanWarps];
   int groups[kInfos];                        // by tile: which 16-token groups were loaded
   uint32_t tmem;
   int abort_flag;
@@ -310,10 +327,74 @@ __device__ __forceinline__ bool find_item(const PromptParams& p, uint32_t x, int
   return false;
 }
 
+// Values of V that are not finite, of tokens that the row at position pos sees and
+// others of its item do not (by a whole warp, a row a thread; pos -1: no row): read
+// again from their pages and added to its outputs in tensor memory. (Out of line, as
+// the next: they hardly ever run, and written in place the whole kernel took 1% longer.)
+__device__ __noinline__ void add_noted(const PromptParams& p, const Notes* notes, uint32_t o_at, int pos) {
+#pragma unroll 1
+  for (int e = 0; e < 4; ++e) {
+    float o[32];
+    tmem_ld32(o_at + 32 * e, o);
+    wait_ld();
+#pragma unroll 1
+    for (int w = 0; w < 2 * kCutTiles * kCleanWarps; ++w) {
+      const Notes& n = notes[w & 1];
+      const int c = w >> 2;
+      uint32_t rows = c < n.count ? n.rows[c][w >> 1 & 1] : 0;
+#pragma unroll 1
+      while (rows) {
+        const int b = 32 * (w >> 1 & 1) + __ffs(rows) - 1, j = n.tok[c] + 16 * (b >> 3) + (b & 7);
+        rows &= rows - 1;
+        if (j > pos || (p.window && j >= p.sinks && j <= pos - p.window)) continue;
+        const int id = p.kv.page_of(n.r, j, nullptr);
+        if (id < 0) continue;
+        const uint4* v = reinterpret_cast<const uint4*>(p.kv.V + p.kv.row(id, n.g, j) + 32 * e);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const uint4 q = v[y];
+          const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            if ((x[z] & 0x7F80u) == 0x7F80u) o[8 * y + 2 * z] += __uint_as_float(x[z] << 16);
+            if ((x[z] & 0x7F800000u) == 0x7F800000u) o[8 * y + 2 * z + 1] += __uint_as_float(x[z] & 0xFFFF0000u);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    tmem_st32(o_at + 32 * e, o);
+  }
+  wait_st();
+}
+
+// Eight rows of V (16 bytes a lane, four rows of a half at v and its fellows) with
+// their values that are not finite cleared, by a whole warp; the rows that had any.
+__device__ __noinline__ uint32_t clear_values(uint4* v) {
+  uint32_t rows = 0;
+#pragma unroll 1
+  for (int y = 0; y < 4; ++y) {
+    uint4& w = v[(y >> 1) * (kHalfBytes / 16) + (y & 1) * 32];
+    uint32_t e[4] = {w.x, w.y, w.z, w.w};
+    bool bad = false;
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      if ((e[z] & 0x7F80u) == 0x7F80u) e[z] &= 0xFFFF0000u, bad = true;
+      if ((e[z] & 0x7F800000u) == 0x7F800000u) e[z] &= 0xFFFFu, bad = true;
+    }
+    if (bad) w = make_uint4(e[0], e[1], e[2], e[3]);
+    const unsigned lanes = __ballot_sync(0xFFFFFFFFu, bad);
+#pragma unroll
+    for (int z = 0; z < 4; ++z)
+      if (lanes >> (8 * z) & 0xFFu) rows |= 1u << (4 * (y & 1) + z);
+  }
+  return rows;
+}
+
 // kTest: every wait is bounded by wait_cycles, and in every block that has as many
 // tiles warp test_warp gives up at tile kTestTile.
 template <bool kPieces, bool kTest = false>
-__global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptParams p,
+__global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_constant__ PromptParams p,
                                                                    const __grid_constant__ CUtensorMap mapQ,
                                                                    const __grid_constant__ CUtensorMap mapK,
                                                                    const __grid_constant__ CUtensorMap mapV) {
@@ -514,24 +595,76 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
           mbar_wait(x & 1 ? &sm.v_full[i % kStages] : &sm.k_full[i % kStages], (i / kStages) & 1, limit);
         }
     } else if (warp >= kCleanWarp) {
-      // ---------------- rows of V that no row of the block sees ----------------
+      // ---------------- what of V must not meet a weight of zero ----------------
+      const int r0 = 8 * (warp - kCleanWarp);  // this warp's rows: eight of every sixteen
       while (ok && take(it, ok)) {
+        Notes& notes = sm.notes[live % kNotes][warp - kCleanWarp];
+        if (it.tiles > 0) {
+          ++live;
+          if (lane == 0) notes.count = 0;
+        }
+        // tokens that some rows have passed, and the first that not every row has come to
+        const int passed0 = max(it.lo, p.sinks), passed1 = p.window ? it.end - p.window : 0, come = it.p_lo + 1;
+        const int cut0 = passed1 > passed0 ? min(passed0, come) : come;
         for (int i = 0; i < it.tiles && ok; ++i, ++at) {
           const int st = at % kStages;
           ok = wait_all(&sm.v_full[st], (at / kStages) & 1);
           if (kTest && p.test_warp == warp && at == kTestTile) ok = false;
           if (!ok) break;
           const int t0 = it.token(i), there = sm.groups[at % kInfos];
-          if (it.ragged(t0, there, p.sinks)) {
-            auto clear = [&](int from, int to) {  // rows of the tile
-              for (int x = 16 * from + tid - 32 * kCleanWarp; x < 16 * to; x += 32 * kCleanWarps)
-                *reinterpret_cast<uint4*>(sm.v[st] + (x >> 3 & 1) * kHalfBytes + (x >> 4) * 128 + (x & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
+          const bool ragged = it.ragged(t0, there, p.sinks);
+          if (ragged) {
+            auto clear = [&](int from, int to) {  // rows of the tile, two a step
+              for (int a = (from & ~15) + r0 + (lane >> 4); a < to; a += 16)
+#pragma unroll
+                for (int y = a; y < a + 8; y += 2)
+                  if (y >= from && y < to)
+                    *reinterpret_cast<uint4*>(sm.v[st] + (lane >> 3 & 1) * kHalfBytes + y * 128 + (lane & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
             };
             for (int e = 0; e < 8; ++e)
               if (!(there >> e & 1)) clear(16 * e, 16 * e + 16);
             if (t0 + kTok > it.end) clear(max(it.end - t0, 0), kTok);
             if (t0 < it.lo) clear(min(max(p.sinks - t0, 0), kTok), min(it.lo - t0, kTok));
+            __syncwarp();
+          }
+          uint32_t rows0 = 0, rows1 = 0;
+          if (t0 + kTok > cut0 && (t0 < passed1 || t0 + kTok > come)) {
+            const int x0 = come - t0, x1 = it.end - t0, y0 = passed0 - t0, y1 = passed1 - t0;
+#pragma unroll 1
+            for (int x = 0; x < 8; ++x) {
+              const int a = 16 * x + r0, b = a + 8;
+              if (max(x0, a) >= min(x1, b) && max(y0, a) >= min(y1, b)) continue;
+              // 16 bytes a lane, four rows of a half at a time
+              uint4* v = reinterpret_cast<uint4*>(sm.v[st] + a * 128) + lane;
+              uint4 w[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) w[y] = v[(y >> 1) * (kHalfBytes / 16) + (y & 1) * 32];
+              __nv_bfloat162 most = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const uint32_t e[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                  most = __hmax2_nan(most, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&e[z])));
+              }
+              const uint32_t m = *reinterpret_cast<const uint32_t*>(&most);
+              if (!__any_sync(0xFFFFFFFFu, (m & 0x7F80u) == 0x7F80u || (m & 0x7F800000u) == 0x7F800000u)) continue;
+              const uint32_t eight = clear_values(v) << (8 * (x & 3));
+              if (x < 4) rows0 |= eight;
+              else rows1 |= eight;
+            }
+          }
+          const bool found = (rows0 | rows1) != 0;
+          if (found && lane == 0) {
+            const int c = notes.count++;
+            notes.r = it.r;
+            notes.g = it.g;
+            notes.tok[c] = t0 + r0;
+            notes.rows[c][0] = rows0;
+            notes.rows[c][1] = rows1;
+          }
+          if (ragged || found) {
             asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
             __syncwarp();
           }
@@ -732,6 +865,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
         ok = ok && done == some;
         live += some;
         fence_after();
+        if (done) {
+          const Notes* notes = sm.notes[(live - 1) % kNotes];
+          if (notes[0].count | notes[1].count) add_noted(p, notes, o_at, there ? pos : -1);
+        }
         if (there) p.part_ml[row] = done ? make_float2(m, l) : make_float2(ninf, 0.f);
 #pragma unroll 1
         for (int e = 0; e < 4 && done; ++e) {
@@ -762,6 +899,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const PromptP
         ok = ok && done == some;
         live += some;
         fence_after();
+        if (done) {
+          const Notes* notes = sm.notes[(live - 1) % kNotes];
+          if (notes[0].count | notes[1].count) add_noted(p, notes, o_at, there ? pos : -1);
+        }
         const float inv = !done ? 0.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
 #pragma unroll 1
         for (int e = 0; e < 2; ++e) {

@@ -509,6 +509,72 @@ def test_prompt_pieces_in_a_graph_and_on_two_streams(kvs):
             assert torch.equal(o, wo) and torch.equal(l, wl)
 
 
+@pytest.mark.parametrize("H", [1, 4, 5, 8])
+@pytest.mark.parametrize("lens,new,window,sinks,wide", [
+    ([700], [700], 0, 0, 0), ([1500, 130, 400], [300, 130, 7], 0, 0, 0), ([700, 900], [700, 300], 100, 0, 0),
+    ([1300], [1300], 300, 70, 0), ([800, 700], [700, 650], 20, 300, 0), ([600, 500], [600, 2], 1, 3, 0), ([6000, 5100], [40, 150], 0, 0, 9000),
+    ([5000, 5000], [300, 64], 3000, 200, 9000)])
+def test_prompt_values_that_are_not_finite_reach_only_those_who_see_them(kvs, H, lens, new, window, sinks, wide):
+    """NaN and infinities in V, in single values and whole rows, in the middle of the queries' own tokens and at the
+    edges of their windows: a query has them in the channels of the rows that it sees and nowhere else, and
+    everything else is bit for bit what it is without them. Whole and split."""
+    G, page = 2, 16
+    k, v, table, n = ref.make(lens, G, page, seed=H + window, poison=False, cap_pages=wide // page or None)
+    cu = [0] + [int(x) for x in np.cumsum(new)]
+    cut = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    q = torch.randn(cu[-1], G * H, D, device=DEV).to(torch.bfloat16)
+    good_v = v.clone()
+    want, wl = kvs.paged_prompt_attn(q, cut, kvs.PagedKV(k, good_v, table, n), window, sinks)
+    ref.check_prompt(want, wl, q, cu, k, good_v, table, lens, window, sinks, SC, G)
+    rng = np.random.default_rng(H + len(lens))
+    inf, nan = float("inf"), float("nan")
+    hit = torch.zeros(len(lens), max(lens), G, D, dtype=torch.bool, device=DEV)
+    for r, (m, c) in enumerate(zip(lens, new)):
+        p0 = m - c
+        at = {p0, m - 1, p0 + c // 2, p0 + c // 3, min(m - 1, p0 + 63), min(m - 1, p0 + 65)}
+        at |= {int(x) for x in rng.integers(p0, m, 6)} | {max(0, p0 - window + 1), max(0, p0 + c // 2 - window)}
+        for i, j in enumerate(sorted(at)):
+            g, d = i % G, int(rng.integers(0, 100))
+            pg = int(table[r, j // page])
+            v[pg, g, j % page, d] = (inf, nan, -inf)[i % 3]
+            if i % 5 == 4:
+                v[pg, g, j % page, 100:] = nan  # many channels of one row
+        rows = torch.stack([v[int(table[r, j // page]), :, j % page] for j in range(m)])
+        hit[r, :m] = ~torch.isfinite(rows)
+    st = _status()
+    out, lse = kvs.paged_prompt_attn(q, cut, kvs.PagedKV(k, v, table, n), window, sinks, dev_status=st)
+    assert int(st) == 0 and torch.equal(lse, wl)
+    for r, (m, c) in enumerate(zip(lens, new)):
+        p = torch.arange(m - c, m, device=DEV).view(-1, 1)
+        j = torch.arange(m, device=DEV)
+        ok = j <= p
+        if window:
+            ok = ok & ((j < sinks) | (j > p - window))
+        # [c][G][D]: some row that the query sees is not finite there
+        bad = torch.einsum("cj,jgd->cgd", ok.double(), hit[r, :m].double()) > 0
+        bad = bad.unsqueeze(2).expand(-1, -1, H, -1).reshape(c, G * H, D)
+        o, w = out[cu[r]:cu[r + 1]], want[cu[r]:cu[r + 1]]
+        assert torch.equal(~torch.isfinite(o.float()), bad), r
+        assert torch.equal(_bits(o)[~bad], _bits(w)[~bad]), r
+        assert bool(bad.any()) and not bool(bad.all())
+
+
+def test_prompt_whole_rows_that_are_not_finite(kvs):
+    """Every V row from a position on is infinite or NaN: the queries before it are as they were."""
+    k, v, table, n = ref.make([500], 1, 64, seed=77, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    cu = torch.tensor([0, 500], dtype=torch.int32, device=DEV)
+    q = torch.randn(500, 4, D, device=DEV).to(torch.bfloat16)
+    want, wl = kvs.paged_prompt_attn(q, cu, cache)
+    for first in (499, 257, 256, 130, 1):
+        for j in range(first, 500):
+            v[int(table[0, j // 64]), :, j % 64] = float("nan") if first % 2 else float("inf")
+        out, lse = kvs.paged_prompt_attn(q, cu, cache)
+        assert torch.equal(_bits(out[:first]), _bits(want[:first])) and torch.equal(lse, wl)
+        assert not bool(torch.isfinite(out[first:].float()).any())
+        assert first % 2 or bool((out[first] == float("inf")).all())
+
+
 def test_prompt_items_that_see_nothing(kvs):
     """Many queries in front of the first token, between items that see something."""
     lens, new, G, H = [3, 260, 0], [900, 260, 500], 8, 8
