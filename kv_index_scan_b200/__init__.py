@@ -593,6 +593,11 @@ def _need(name: str, t, shape, dtype, dev):
     return t
 
 
+def _ws_args(ws):
+    """A workspace's pointer and size; None where the library asks for none (or refuses the call's sizes)."""
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+
+
 def _check_ws(ws, dev):
     if not (ws.device == dev and ws.dtype is torch.uint8 and ws.is_contiguous()):
         raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
@@ -623,6 +628,7 @@ class PagedKV:
             _require(t.stride(-1) == 1 or t.shape[-1] == 1, f"{name} must be contiguous in its last dimension")
         _require(k_pages.shape == v_pages.shape and k_pages.stride() == v_pages.stride(),
                  "k_pages and v_pages must have the same shape and strides")
+        _require(k_pages.numel() > 0, f"k_pages must not be empty, got {tuple(k_pages.shape)}")
         self.num_pages, self.G, self.page, self.D = k_pages.shape
         self.R, self.max_pages = table.shape
         _require(n.shape[0] == self.R, f"n must have {self.R} entries, got {n.shape[0]}")
@@ -720,7 +726,7 @@ def paged_decode_attn(q: torch.Tensor, cache: PagedKV, window: int = 0, sinks: i
         _check_ws(ws, dev)
     a = PagedDecodeArgsC(cache._ref, q.data_ptr(), KVS_BF16 if bf16 else KVS_F32, H, window, sinks,
                          1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), lse.data_ptr(), mp, mo)
-    _check(_lib.paged_decode_attn(ctypes.byref(a), ws.data_ptr(), ws.numel(), _ptr(dev_status), _raw_stream(dev)),
+    _check(_lib.paged_decode_attn(ctypes.byref(a), *_ws_args(ws), _ptr(dev_status), _raw_stream(dev)),
            "paged_decode_attn")
     return out, lse
 
@@ -736,7 +742,7 @@ def selftest_paged_decode_timeout(q: torch.Tensor, cache: PagedKV, warp: int, wa
         out = torch.empty(q.shape, dtype=torch.float32, device=dev)
         ws = paged_decode_workspace(cache, H)
         a = PagedDecodeArgsC(cache._ref, q.data_ptr(), KVS_BF16, H, 0, 0, 1.0, out.data_ptr(), None, None, None)
-        _check(_lib.kvs_selftest_paged_decode_timeout(ctypes.byref(a), ws.data_ptr(), ws.numel(), warp, wait_cycles,
+        _check(_lib.kvs_selftest_paged_decode_timeout(ctypes.byref(a), *_ws_args(ws), warp, wait_cycles,
                                                       _ptr(dev_status), _raw_stream(dev)),
                "kvs_selftest_paged_decode_timeout")
 
@@ -778,11 +784,8 @@ def paged_prompt_attn(q: torch.Tensor, cu: torch.Tensor, cache: PagedKV, window:
                               sinks)
     else:
         _check_ws(ws, dev)
-    if ws is None:
-        wp = wn = 0
-    else:
-        wp, wn = ws.data_ptr(), ws.numel()
-    _check(_lib.paged_prompt_attn(ctypes.byref(a), wp, wn, _ptr(dev_status), _raw_stream(dev)), "paged_prompt_attn")
+    _check(_lib.paged_prompt_attn(ctypes.byref(a), *_ws_args(ws), _ptr(dev_status), _raw_stream(dev)),
+           "paged_prompt_attn")
     return out, lse
 
 
@@ -836,6 +839,6 @@ def paged_evict(cache: PagedKV, mass: torch.Tensor, budget: int, sinks: int = 0,
     else:
         _check_ws(ws, dev)
     a = PagedEvictArgsC(cache._ref, mp, pp, sp, budget, sinks, recent, mo, po, no, src.data_ptr())
-    _check(_lib.kvs_paged_evict(ctypes.byref(a), ws.data_ptr(), ws.numel(), _ptr(dev_status),
-                                _raw_stream(dev)), "kvs_paged_evict")
+    _check(_lib.kvs_paged_evict(ctypes.byref(a), *_ws_args(ws), _ptr(dev_status), _raw_stream(dev)),
+           "kvs_paged_evict")
     return src

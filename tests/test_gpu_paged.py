@@ -394,6 +394,22 @@ def test_binding_refusals(kvs):
             call()
 
 
+def test_no_heads_and_no_pages_are_refused(kvs):
+    """No query heads in any call, and pools of no pages, heads or tokens."""
+    k, v, table, n = ref.make([20], 2, 16, seed=1)
+    cache = kvs.PagedKV(k, v, table, n)
+    cu = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    for call in (lambda: kvs.paged_decode_attn(torch.empty(1, 2, 0, D, device=DEV), cache),
+                 lambda: kvs.paged_decode_attn(torch.empty(1, 2, 0, D, device=DEV), cache,
+                                               mass=torch.zeros(1, 2, cache.cap, device=DEV)),
+                 lambda: kvs.paged_prompt_attn(torch.empty(1, 0, D, dtype=torch.bfloat16, device=DEV), cu, cache)):
+        with pytest.raises(kvs.KvsError, match="H=0"):
+            call()
+    for none in (k[:0], k[:, :0], k[:, :, :0]):
+        with pytest.raises(ValueError, match="empty"):
+            kvs.PagedKV(none, none, table, n)
+
+
 # ----------------------------------------------------------------------------- prompt
 
 def _prompt(kvs, lens, new, G, H, page, window, sinks, seed=0, pad=3, layout="head", poison=True):
