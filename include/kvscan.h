@@ -489,7 +489,8 @@ KVS_API kvs_status kvs_paged_append(const kvs_paged_kv* kv, const uint16_t* Knew
  * out = sum_j softmax(l)_j V_j and lse = log sum_j exp(l_j). A request with no
  * visible token gets out = 0 and lse = -inf.
  *   q f32 or bf16 [R][G][H][D]; out f32 [R][G][H][D]; lse (nullable) f32
- *   [R][G][H]. H in 1..8; scale finite and not 0 (in both attentions).
+ *   [R][G][H]. H in 1..8; scale not 0 and at most 2.3e38 in magnitude (in
+ *   both attentions).
  * mass, mass_out (both or neither) f32 [R][G][max_pages * page]: for every
  * visible token mass_out[j] = mass[j] + sum_h softmax(l)_hj; the other entries
  * of mass_out stay as they are. mass_out may be mass itself, or not overlap it.

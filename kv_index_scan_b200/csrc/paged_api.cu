@@ -54,8 +54,9 @@ kvs_status check_paged(const char* who, const kvs_paged_kv* kv) {
 }
 
 kvs_status check_mask(const char* who, int window, int sinks, float scale) {
-  KVS_REQUIRE(std::isfinite(scale) && scale != 0.f, KVS_EINVAL, "%s: scale=%g must be finite and not 0", who,
-              static_cast<double>(scale));
+  // (the softmax is in base 2, so scale * log2(e) has to be finite too)
+  KVS_REQUIRE(std::isfinite(scale * 1.4426950408889634f) && scale != 0.f, KVS_EINVAL,
+              "%s: scale=%g must not be 0, and at most 2.3e38 in magnitude", who, static_cast<double>(scale));
   KVS_REQUIRE(window >= 0 && sinks >= 0, KVS_EINVAL, "%s: window=%d sinks=%d must not be negative", who, window,
               sinks);
   return KVS_OK;

@@ -160,3 +160,15 @@ def test_prompt_timeout_selftest_checks(kvs):
     for bad in (dict(warp=-1), dict(warp=12), dict(cycles=999), dict(cycles=3 * 10 ** 9), dict(status=None), dict(T=0),
                 dict(out=None)):
         assert call(**bad) == kvs.KVS_EINVAL, bad
+
+
+@pytest.mark.parametrize("scale", [3e38, -3e38, 2.4e38, float("inf"), float("-inf"), float("nan"), 0.0])
+def test_scales_without_a_finite_base_2_form_are_refused(kvs, scale):
+    """The kernels multiply by scale * log2(e): where that is not finite a logit of 0 would become NaN."""
+    kv = _kv(kvs)
+    d = kvs.PagedDecodeArgsC(ctypes.pointer(kv), 4096, 0, 4, 0, 0, scale, 4096, None, None, None)
+    assert kvs._lib.paged_decode_attn(ctypes.byref(d), 4096, 1 << 40, None, None) == kvs.KVS_EINVAL
+    assert b"scale" in kvs._lib.kvs_last_error()
+    p = kvs.PagedPromptArgsC(ctypes.pointer(kv), 4096, 1024, 4096, 4, 4, 0, 0, scale, 4096, 1024, None)
+    assert kvs._lib.paged_prompt_attn(ctypes.byref(p), 4096, 1 << 40, None, None) == kvs.KVS_EINVAL
+    assert b"scale" in kvs._lib.kvs_last_error()
