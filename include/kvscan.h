@@ -542,7 +542,10 @@ KVS_API kvs_status kvs_selftest_paged_decode_timeout(const kvs_paged_decode_args
  * all of theirs.
  * Workspace: kvs_paged_prompt_workspace_size(R, G, H, T, max_pages * page, window,
  * sinks), which is 0 where there are queries enough to occupy the GPU; fewer are
- * split over the tokens they see, and the parts joined. */
+ * split over the tokens they see, and the parts joined. So it does not grow with T:
+ * a workspace for calls of different T has to have
+ * kvs_paged_prompt_workspace_bound, the most that any call of 1 to T queries asks
+ * for with the other arguments as they are. */
 typedef struct {
   const kvs_paged_kv* kv;
   const uint16_t* q;
@@ -559,6 +562,8 @@ KVS_API kvs_status paged_prompt_attn(const kvs_paged_prompt_args* a, void* ws, s
                                      int32_t* dev_status, void* stream);
 KVS_API size_t kvs_paged_prompt_workspace_size(int32_t R, int32_t G, int32_t H, int32_t T, int32_t cap,
                                                int32_t window, int32_t sinks);
+KVS_API size_t kvs_paged_prompt_workspace_bound(int32_t R, int32_t G, int32_t H, int32_t T, int32_t cap,
+                                                int32_t window, int32_t sinks);
 
 /* kvs_selftest_paged_prompt_timeout -- the same check for paged_prompt_attn
  * (not split): in every block with two tiles of 128 tokens or more to do, warp

@@ -134,6 +134,8 @@ def _declare():
     L.paged_prompt_attn.restype = I32
     L.kvs_paged_prompt_workspace_size.argtypes = [I32] * 7
     L.kvs_paged_prompt_workspace_size.restype = SZ
+    L.kvs_paged_prompt_workspace_bound.argtypes = [I32] * 7
+    L.kvs_paged_prompt_workspace_bound.restype = SZ
     L.kvs_selftest_paged_prompt_timeout.argtypes = [ctypes.POINTER(PagedPromptArgsC), I32, I64, P, P]
     L.kvs_selftest_paged_prompt_timeout.restype = I32
     L.kvs_paged_evict.argtypes = [ctypes.POINTER(PagedEvictArgsC), P, SZ, P, P]
@@ -745,6 +747,25 @@ def selftest_paged_decode_timeout(q: torch.Tensor, cache: PagedKV, warp: int, wa
         _check(_lib.kvs_selftest_paged_decode_timeout(ctypes.byref(a), *_ws_args(ws), warp, wait_cycles,
                                                       _ptr(dev_status), _raw_stream(dev)),
                "kvs_selftest_paged_decode_timeout")
+
+
+def paged_prompt_workspace(cache: PagedKV, H: int, T: int, window: int = 0, sinks: int = 0):
+    """A workspace for every paged_prompt_attn of up to T queries with H query heads a KV head, this window and
+    these sinks, for callers that keep one (None: no such call needs any)."""
+    if _elsewhere(cache.device, None):
+        with _on(cache.device, None):
+            return paged_prompt_workspace(cache, H, T, window, sinks)
+    _counts(H=H, T=T, window=window, sinks=sinks)
+    return cache._workspace("kvs_paged_prompt_workspace_bound", H, T, cache.cap, window, sinks)
+
+
+def paged_evict_workspace(cache: PagedKV, budget: int) -> torch.Tensor:
+    """A workspace for paged_evict down to `budget` or less, for callers that keep one."""
+    if _elsewhere(cache.device, None):
+        with _on(cache.device, None):
+            return paged_evict_workspace(cache, budget)
+    _counts(budget=budget)
+    return cache._workspace("kvs_paged_evict_workspace_size", budget)
 
 
 def paged_prompt_attn(q: torch.Tensor, cu: torch.Tensor, cache: PagedKV, window: int = 0, sinks: int = 0,

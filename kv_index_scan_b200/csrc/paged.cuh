@@ -69,6 +69,7 @@ size_t paged_decode_ws_bytes(int R, int G, int H, int weight_cap);
 kvs_status paged_decode_launch(const kvs_paged_decode_args* a, void* ws, int32_t* dev_status, cudaStream_t s,
                                int test_warp = -1, int64_t wait_cycles = 0);
 size_t paged_prompt_ws_bytes(int R, int G, int H, int T, int cap, int window, int sinks);
+size_t paged_prompt_ws_bound(int R, int G, int H, int T, int cap, int window, int sinks);  // over 1 .. T queries
 // (likewise: kvs_selftest_paged_prompt_timeout)
 kvs_status paged_prompt_launch(const kvs_paged_prompt_args* a, void* ws, int32_t* dev_status, cudaStream_t s,
                                int test_warp = -1, int64_t wait_cycles = 0);

@@ -148,6 +148,11 @@ size_t kvs_paged_prompt_workspace_size(int32_t R, int32_t G, int32_t H, int32_t 
   return paged_prompt_ws_bytes(R, G, H, T, cap, window, sinks);
 }
 
+size_t kvs_paged_prompt_workspace_bound(int32_t R, int32_t G, int32_t H, int32_t T, int32_t cap, int32_t window,
+                                        int32_t sinks) {
+  return paged_prompt_ws_bound(R, G, H, T, cap, window, sinks);
+}
+
 kvs_status paged_prompt_attn(const kvs_paged_prompt_args* a, void* ws, size_t ws_bytes, int32_t* dev_status,
                              void* stream) {
   KVS_PROPAGATE(check_prompt(a));

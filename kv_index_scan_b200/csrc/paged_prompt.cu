@@ -47,6 +47,7 @@
 // winds down with no copy in flight and its tensor memory freed.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cstring>
 #include <type_traits>
 
@@ -983,19 +984,24 @@ int64_t most_items(int R, int G, int H, int T) {
   return (T + (T < R ? T : R) * (per2 - 1)) / per2 * G;
 }
 
-// Pieces that an item's tiles are split in. In units of a tile's time (1.75 us),
-// with t tiles in the longest item that there may be, a round of whole items
-// takes t + 3.5, one of n pieces t / n + 5, and the join 4 (8 heads, 4 tokens over
-// 28676: 359 us whole, 37 in 18 pieces; 2 heads, 1024 tokens: 20.6 whole, 23.1 in
-// two): the number with the least sum of rounds.
-int pieces_of(int R, int G, int H, int T, int64_t cap, int window, int sinks) {
-  const int64_t items = most_items(R, G, H, T), sms = sm_count();
+// Tiles of the longest item that there may be.
+int64_t longest_item(int H, int64_t cap, int window, int sinks) {
   int64_t t = (cap + kTok - 1) / kTok;
   if (window) {
     const int64_t seen = (static_cast<int64_t>(window) + 2 * (kRows / H) + kTok - 1) / kTok + 1 +
                          (static_cast<int64_t>(sinks) + kTok - 1) / kTok;
     if (seen < t) t = seen;
   }
+  return t;
+}
+
+// Pieces that an item's tiles are split in. In units of a tile's time (1.75 us),
+// with t tiles in the longest item that there may be, a round of whole items
+// takes t + 3.5, one of n pieces t / n + 5, and the join 4 (8 heads, 4 tokens over
+// 28676: 359 us whole, 37 in 18 pieces; 2 heads, 1024 tokens: 20.6 whole, 23.1 in
+// two): the number with the least sum of rounds.
+int pieces_of(int R, int G, int H, int T, int64_t cap, int window, int sinks) {
+  const int64_t items = most_items(R, G, H, T), sms = sm_count(), t = longest_item(H, cap, window, sinks);
   int best = 1;
   double least = static_cast<double>((items + sms - 1) / sms) * (t + 3.5);
   for (int n = 2; n <= kMaxPieces && n * kPieceTiles <= t; ++n) {
@@ -1026,6 +1032,24 @@ size_t carve(PromptParams* p, void* ws, int G, int H, int T, int pieces) {
 size_t paged_prompt_ws_bytes(int R, int G, int H, int T, int cap, int window, int sinks) {
   if (R < 1 || G < 1 || H < 1 || H > 8 || T < 1) return 0;
   return carve(nullptr, nullptr, G, H, T, pieces_of(R, G, H, T, cap, window, sinks));
+}
+
+// The workspace grows with T as long as the items, and so the pieces, stay the same:
+// the last T of each number of items is asked. With items * 6.5 >= sms * t one piece
+// is the least for good (n pieces cost at least items / sms * (t + 5 n) + 4).
+size_t paged_prompt_ws_bound(int R, int G, int H, int T, int cap, int window, int sinks) {
+  if (R < 1 || G < 1 || H < 1 || H > 8 || T < 1) return 0;
+  const int64_t per2 = 2 * (kRows / H), t = longest_item(H, cap, window, sinks), sms = sm_count();
+  size_t most = 0;
+  for (int64_t x = 1; x <= T; ++x) {
+    if (x >= R) {
+      const int64_t empty = R * (per2 - 1), blocks = (x + empty) / per2;
+      x = std::min<int64_t>(T, (blocks + 1) * per2 - empty - 1);
+    }
+    most = std::max(most, paged_prompt_ws_bytes(R, G, H, static_cast<int>(x), cap, window, sinks));
+    if (6.5 * most_items(R, G, H, static_cast<int>(x)) >= static_cast<double>(sms) * t) break;
+  }
+  return most;
 }
 
 kvs_status paged_prompt_launch(const kvs_paged_prompt_args* a, void* ws, int32_t* dev_status, cudaStream_t s,

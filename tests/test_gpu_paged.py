@@ -591,6 +591,30 @@ def test_prompt_whole_rows_that_are_not_finite(kvs):
         assert first % 2 or bool((out[first] == float("inf")).all())
 
 
+def test_kept_workspaces_serve_calls_of_other_sizes(kvs):
+    """One workspace for prompts of few queries (split) and many (whole), one for evictions to smaller budgets."""
+    lens, G, H = [9000, 700], 2, 4
+    k, v, table, n = ref.make(lens, G, 64, seed=53, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    ws = kvs.paged_prompt_workspace(cache, H, 700)
+    for new in ([3, 0], [100, 40], [500, 200], [1, 1]):
+        cu = [0] + [int(x) for x in np.cumsum(new)]
+        q = torch.randn(cu[-1], G * H, D, device=DEV).to(torch.bfloat16)
+        cut = torch.tensor(cu, dtype=torch.int32, device=DEV)
+        out, lse = kvs.paged_prompt_attn(q, cut, cache, ws=ws)
+        ref.check_prompt(out, lse, q, cu, k, v, table, lens, 0, 0, SC, G)
+    assert kvs.paged_prompt_workspace(cache, H, 700, window=50) is None
+    mass = torch.rand(2, G, cache.cap, device=DEV)
+    we = kvs.paged_evict_workspace(cache, 600)
+    for budget in (600, 77):
+        mo, no = torch.zeros_like(mass), torch.zeros_like(n)
+        src = kvs.paged_evict(cache, mass, budget, mass_out=mo, n_out=no, ws=we)
+        for r in range(2):
+            for g in range(G):
+                want = ref.evict(mass[r, g].cpu().numpy(), np.arange(cache.cap), lens[r], lens[r], budget, 0, 0)
+                assert np.array_equal(src[r, g].cpu().numpy()[:len(want)], want)
+
+
 def test_prompt_items_that_see_nothing(kvs):
     """Many queries in front of the first token, between items that see something."""
     lens, new, G, H = [3, 260, 0], [900, 260, 500], 8, 8

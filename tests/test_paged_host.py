@@ -172,3 +172,25 @@ def test_scales_without_a_finite_base_2_form_are_refused(kvs, scale):
     p = kvs.PagedPromptArgsC(ctypes.pointer(kv), 4096, 1024, 4096, 4, 4, 0, 0, scale, 4096, 1024, None)
     assert kvs._lib.paged_prompt_attn(ctypes.byref(p), 4096, 1 << 40, None, None) == kvs.KVS_EINVAL
     assert b"scale" in kvs._lib.kvs_last_error()
+
+
+@pytest.mark.parametrize("R,G,H,T,cap,window,sinks", [
+    (1, 1, 4, 700, 65536, 0, 0), (2, 2, 4, 900, 65536, 0, 0), (40, 8, 8, 500, 131072, 0, 0), (3, 8, 1, 3000, 30000, 0, 0),
+    (1, 8, 5, 2500, 200000, 9000, 300), (64, 1, 3, 400, 16384, 0, 0), (2, 2, 4, 900, 128, 0, 0), (1, 4, 4, 1, 65536, 0, 0)])
+def test_prompt_workspace_bound(kvs, R, G, H, T, cap, window, sinks):
+    """A workspace of the bound is enough for every call of up to T queries, and one of them needs all of it; the
+    size of a call itself falls to 0 where queries are many."""
+    size = kvs._lib.kvs_paged_prompt_workspace_size
+    bound = kvs._lib.kvs_paged_prompt_workspace_bound(R, G, H, T, cap, window, sinks)
+    assert bound == max(size(R, G, H, t, cap, window, sinks) for t in range(1, T + 1))
+    assert bound >= kvs._lib.kvs_paged_prompt_workspace_bound(R, G, H, max(1, T // 3), cap, window, sinks)
+
+
+def test_prompt_workspace_bound_of_many_queries(kvs):
+    """Beyond the last split call more queries change nothing; sizes that no call takes ask for nothing."""
+    bound = kvs._lib.kvs_paged_prompt_workspace_bound
+    assert kvs._lib.kvs_paged_prompt_workspace_size(1, 8, 4, 1 << 20, 65536, 0, 0) == 0
+    assert bound(1, 8, 4, 1 << 20, 65536, 0, 0) == bound(1, 8, 4, 1 << 16, 65536, 0, 0) > 0
+    for bad in ((0, 8, 4, 9, 65536, 0, 0), (1, 0, 4, 9, 65536, 0, 0), (1, 8, 0, 9, 65536, 0, 0), (1, 8, 9, 9, 65536, 0, 0),
+                (1, 8, 4, 0, 65536, 0, 0)):
+        assert bound(*bad) == 0
