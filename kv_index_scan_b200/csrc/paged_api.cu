@@ -66,9 +66,9 @@ kvs_status check_decode(const kvs_paged_decode_args* a, const void* ws, size_t w
   KVS_REQUIRE(a != nullptr, KVS_EINVAL, "paged_decode_attn: args is null");
   KVS_PROPAGATE(check_paged("paged_decode_attn", a->kv));
   KVS_PROPAGATE(check_mask("paged_decode_attn", a->window, a->sinks, a->scale));
+  KVS_REQUIRE(a->H >= 1 && a->H <= 8, KVS_EINVAL, "paged_decode_attn: H=%d query heads per KV head (1..8)", a->H);
   KVS_REQUIRE(a->q && a->out, KVS_EINVAL, "paged_decode_attn: q and out must be non-null");
   KVS_REQUIRE(a->q_dtype == KVS_F32 || a->q_dtype == KVS_BF16, KVS_EINVAL, "paged_decode_attn: q_dtype=%d", a->q_dtype);
-  KVS_REQUIRE(a->H >= 1 && a->H <= 8, KVS_EINVAL, "paged_decode_attn: H=%d query heads per KV head (1..8)", a->H);
   KVS_REQUIRE(aligned16(a->q) && aligned16(a->out), KVS_EINVAL, "paged_decode_attn: q and out must be 16-byte aligned");
   KVS_REQUIRE((a->mass == nullptr) == (a->mass_out == nullptr), KVS_EINVAL,
               "paged_decode_attn: mass and mass_out go together");
