@@ -612,14 +612,33 @@ def _counts(**values):
             raise ValueError(f"{name} must be an int from 0 to 2^31 - 1, got {v!r}")
 
 
+class _Kept:
+    """An attribute whose tensor a C descriptor points to: assigning another one would leave the descriptor with
+    the memory of the first, so it is refused (`x.n += 1` assigns the same tensor, and is not)."""
+
+    def __init__(self, name: str):
+        self.name = name
+
+    def __get__(self, obj, cls=None):
+        return self if obj is None else obj.__dict__[self.name]
+
+    def __set__(self, obj, t):
+        _require(obj.__dict__.get(self.name, t) is t,
+                 f"{self.name} stays the tensor it was made with: change that one in place (.copy_), or make another cache")
+        obj.__dict__[self.name] = t
+
+
 class PagedKV:
     """A paged K/V cache (tensors owned by torch).
 
     k_pages, v_pages bf16 [num_pages][G][page][128], of the same strides, the last dimension contiguous
     (a pool laid out [num_pages][page][G][128] is passed as its .transpose(1, 2)); table int32
     [R][max_pages], the pages of each request in order; n int32 [R], the tokens each holds. The tensors
-    are read by later calls as they are then: n and table may change in place, in a captured graph too.
+    are read by later calls as they are then: n and table may change in place, in a captured graph too. The
+    attributes k_pages, v_pages, table and n stay these tensors; others make another PagedKV.
     """
+
+    k_pages, v_pages, table, n = (_Kept(x) for x in ("k_pages", "v_pages", "table", "n"))
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, n: torch.Tensor):
         for name, t, dt, dims in (("k_pages", k_pages, torch.bfloat16, 4), ("v_pages", v_pages, torch.bfloat16, 4),

@@ -394,6 +394,23 @@ def test_binding_refusals(kvs):
             call()
 
 
+def test_a_cache_keeps_its_tensors(kvs):
+    """n and table change in place; another tensor in their place, which no call would read, is refused."""
+    k, v, table, n = ref.make([20, 33], 2, 16, seed=1, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    for name, t in (("n", n + 1), ("table", table.clone()), ("k_pages", k.clone()), ("v_pages", v.clone())):
+        with pytest.raises(ValueError, match=name):
+            setattr(cache, name, t)
+    assert cache.n is n and cache.table is table and cache.k_pages is k and cache.v_pages is v
+    cache.n -= 3
+    q = torch.randn(2, 2, 4, D, device=DEV)
+    out, lse = kvs.paged_decode_attn(q, cache)
+    ref.check_decode(out, lse, q, k, v, table, [17, 30], 0, 0, SC)
+    cache.n.copy_(torch.tensor([5, 6]))
+    out, lse = kvs.paged_decode_attn(q, cache)
+    ref.check_decode(out, lse, q, k, v, table, [5, 6], 0, 0, SC)
+
+
 def test_no_heads_and_no_pages_are_refused(kvs):
     """No query heads in any call, and pools of no pages, heads or tokens."""
     k, v, table, n = ref.make([20], 2, 16, seed=1)
