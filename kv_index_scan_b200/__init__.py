@@ -605,6 +605,16 @@ def _check_ws(ws, dev):
         raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
 
 
+def _status_ptr(t, dev):
+    """The status word's address. Kernels write there, so a tensor of another type or in ordinary host memory is
+    refused (a raw address is the caller's word)."""
+    if isinstance(t, torch.Tensor) and not (t.dtype is torch.int32 and t.numel() >= 1
+                                            and (t.device == dev or (t.device.type == "cpu" and t.is_pinned()))):
+        raise ValueError(f"dev_status must be an int32 tensor on {dev} or in pinned host memory, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return _ptr(t)
+
+
 def _counts(**values):
     """Every value fits the C boundary's int32 and is not negative."""
     for name, v in values.items():
@@ -624,7 +634,8 @@ class _Kept:
 
     def __set__(self, obj, t):
         _require(obj.__dict__.get(self.name, t) is t,
-                 f"{self.name} stays the tensor it was made with: change that one in place (.copy_), or make another cache")
+                 f"{self.name} stays the tensor it was made with: change that one in place (.copy_), or make another "
+                 "cache")
         obj.__dict__[self.name] = t
 
 
@@ -701,8 +712,9 @@ def paged_append(cache: PagedKV, Knew: torch.Tensor, Vnew: torch.Tensor, cu=None
     cup = None if cu is None else _need("cu", cu, cache._cu_shape, torch.int32, dev).data_ptr()
     sp = None if seen is None else _need("seen", seen, cache._r_shape, torch.int32, dev).data_ptr()
     mp, pp = cache._state("mass", mass, torch.float32), cache._state("pos", pos, torch.int32)
+    st_ptr = None if dev_status is None else _status_ptr(dev_status, dev)
     _check(_lib.kvs_paged_append(cache._ref, Knew.data_ptr(), Vnew.data_ptr(), ld, cup, T, mp, pp, sp,
-                                 _ptr(dev_status), _raw_stream(dev)), "kvs_paged_append")
+                                 st_ptr, _raw_stream(dev)), "kvs_paged_append")
 
 
 def paged_decode_workspace(cache: PagedKV, H: int, weights: bool = False) -> torch.Tensor:
@@ -747,7 +759,8 @@ def paged_decode_attn(q: torch.Tensor, cache: PagedKV, window: int = 0, sinks: i
         _check_ws(ws, dev)
     a = PagedDecodeArgsC(cache._ref, q.data_ptr(), KVS_BF16 if bf16 else KVS_F32, H, window, sinks,
                          1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), lse.data_ptr(), mp, mo)
-    _check(_lib.paged_decode_attn(ctypes.byref(a), *_ws_args(ws), _ptr(dev_status), _raw_stream(dev)),
+    st_ptr = None if dev_status is None else _status_ptr(dev_status, dev)
+    _check(_lib.paged_decode_attn(ctypes.byref(a), *_ws_args(ws), st_ptr, _raw_stream(dev)),
            "paged_decode_attn")
     return out, lse
 
@@ -764,7 +777,7 @@ def selftest_paged_decode_timeout(q: torch.Tensor, cache: PagedKV, warp: int, wa
         ws = paged_decode_workspace(cache, H)
         a = PagedDecodeArgsC(cache._ref, q.data_ptr(), KVS_BF16, H, 0, 0, 1.0, out.data_ptr(), None, None, None)
         _check(_lib.kvs_selftest_paged_decode_timeout(ctypes.byref(a), *_ws_args(ws), warp, wait_cycles,
-                                                      _ptr(dev_status), _raw_stream(dev)),
+                                                      _status_ptr(dev_status, dev), _raw_stream(dev)),
                "kvs_selftest_paged_decode_timeout")
 
 
@@ -824,7 +837,8 @@ def paged_prompt_attn(q: torch.Tensor, cu: torch.Tensor, cache: PagedKV, window:
                               sinks)
     else:
         _check_ws(ws, dev)
-    _check(_lib.paged_prompt_attn(ctypes.byref(a), *_ws_args(ws), _ptr(dev_status), _raw_stream(dev)),
+    st_ptr = None if dev_status is None else _status_ptr(dev_status, dev)
+    _check(_lib.paged_prompt_attn(ctypes.byref(a), *_ws_args(ws), st_ptr, _raw_stream(dev)),
            "paged_prompt_attn")
     return out, lse
 
@@ -842,7 +856,7 @@ def selftest_paged_prompt_timeout(q: torch.Tensor, cu: torch.Tensor, cache: Page
         out = torch.empty_like(q)
         a = PagedPromptArgsC(cache._ref, q.data_ptr(), Hq * D, cu.data_ptr(), T, Hq // cache.G, 0, 0, 1.0,
                              out.data_ptr(), Hq * D, None)
-        _check(_lib.kvs_selftest_paged_prompt_timeout(ctypes.byref(a), warp, wait_cycles, _ptr(dev_status),
+        _check(_lib.kvs_selftest_paged_prompt_timeout(ctypes.byref(a), warp, wait_cycles, _status_ptr(dev_status, dev),
                                                       _raw_stream(dev)), "kvs_selftest_paged_prompt_timeout")
 
 
@@ -879,6 +893,7 @@ def paged_evict(cache: PagedKV, mass: torch.Tensor, budget: int, sinks: int = 0,
     else:
         _check_ws(ws, dev)
     a = PagedEvictArgsC(cache._ref, mp, pp, sp, budget, sinks, recent, mo, po, no, src.data_ptr())
-    _check(_lib.kvs_paged_evict(ctypes.byref(a), *_ws_args(ws), _ptr(dev_status), _raw_stream(dev)),
+    st_ptr = None if dev_status is None else _status_ptr(dev_status, dev)
+    _check(_lib.kvs_paged_evict(ctypes.byref(a), *_ws_args(ws), st_ptr, _raw_stream(dev)),
            "kvs_paged_evict")
     return src

@@ -394,6 +394,27 @@ def test_binding_refusals(kvs):
             call()
 
 
+def test_status_words_elsewhere_are_refused(kvs):
+    """A status word in ordinary host memory, of another type or empty, in every call (none is launched)."""
+    k, v, table, n = ref.make([20], 2, 16, seed=1, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    q, cu = torch.randn(1, 2, 4, D, device=DEV), torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    qp, mass = q.view(1, 8, D).bfloat16(), torch.zeros(1, 2, cache.cap, device=DEV)
+    for st in (torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int64, device=DEV),
+               torch.zeros(0, dtype=torch.int32, device=DEV)):
+        for call in (lambda: kvs.paged_append(cache, qp[:, :2], qp[:, 2:4], dev_status=st),
+                     lambda: kvs.paged_decode_attn(q, cache, dev_status=st),
+                     lambda: kvs.paged_prompt_attn(qp, cu, cache, dev_status=st),
+                     lambda: kvs.paged_evict(cache, mass, 8, dev_status=st)):
+            with pytest.raises(ValueError, match="dev_status"):
+                call()
+    assert n.tolist() == [20]
+    pinned = torch.zeros(1, dtype=torch.int32).pin_memory()
+    kvs.paged_decode_attn(q, cache, dev_status=pinned)
+    torch.cuda.synchronize()
+    assert int(pinned) == 0
+
+
 def test_a_cache_keeps_its_tensors(kvs):
     """n and table change in place; another tensor in their place, which no call would read, is refused."""
     k, v, table, n = ref.make([20, 33], 2, 16, seed=1, poison=False)
