@@ -473,8 +473,9 @@ typedef struct {
  * ascending; NULL: one each, T = R), packed row cu[r] + t goes to position
  * i = n[r] - c + t. Knew, Vnew bf16 [T][G][D] with rows new_ld elements apart
  * from token to token (a multiple of 8) and D from head to head; packed rows
- * from cu[R] on are not read. Positions outside 0 .. max_pages * page - 1 are
- * not written (KVS_EBOUNDS). mass (nullable) f32 [R][G][max_pages * page] and
+ * from cu[R] on have no influence. Positions outside 0 .. max_pages * page - 1
+ * are not written, nor rows that the offsets give to no request because they do
+ * not begin at 0 or do not ascend, nor rows from T on (KVS_EBOUNDS). mass (nullable) f32 [R][G][max_pages * page] and
  * pos (nullable) int32 of the same shape get, at i, 0 and the token's place in
  * the request: seen[r] - c + t with seen (nullable device int32 [R]) the
  * tokens that the request has had in all, these included; i without it. */
@@ -532,8 +533,8 @@ KVS_API kvs_status kvs_selftest_paged_decode_timeout(const kvs_paged_decode_args
  *   q bf16 [T][G*H][D] (query heads g*H .. g*H + H-1 share KV head g), tokens
  *   q_ld elements apart; out bf16 likewise with out_ld; lse (nullable) f32
  *   [T][G*H]. H in 1..8; q_ld, out_ld multiples of 8, q and out 16-byte
- *   aligned. Packed rows from cu[R] on are neither read nor written; a query
- *   that sees nothing (p < 0) gets out = 0 and lse = -inf. Entries of cu
+ *   aligned. All T rows of q are there; those from cu[R] on have no influence,
+ *   and of out and lse they are left as they are. A query that sees nothing (p < 0) gets out = 0 and lse = -inf. Entries of cu
  *   outside 0 .. T are clamped (KVS_EBOUNDS).
  * The softmax and all sums are f32; the weights are rounded to bf16 for the
  * product with V, and out once at the end. K and V rows that a query does not

@@ -50,9 +50,15 @@ __global__ void __launch_bounds__(32 * kAppendWarps) paged_append_kernel(
     if (g0 + h < g1) v[h] = __ldg(reinterpret_cast<const uint4*>(from + (g0 + h) * kD));
   int r = t, behind = 1;  // tokens of the request from this one on
   if (cu) {
+    if (item == 0 && __ldg(cu + kv.R) > T) set_status(dev_status, KVS_EBOUNDS);  // rows that are not there
     r = request_of(cu, kv.R, t, lane);
     if (r < 0) return;
+    const int first = __ldg(cu + r);
     behind = __ldg(cu + r + 1) - t;
+    if (behind <= 0 || first > t) {  // offsets that do not begin at 0 or do not ascend: nobody's row
+      set_status(dev_status, KVS_EBOUNDS);
+      return;
+    }
   }
   const int i = kv.n[r] - behind;
   if (i < 0 || i >= kv.cap()) {

@@ -89,6 +89,25 @@ def test_append_refuses_positions_and_pages_that_are_none(kvs):
     assert torch.equal(_bits(k), _bits(wk)) and torch.equal(_bits(v), _bits(wv))
 
 
+@pytest.mark.parametrize("cu,written", [
+    ([0, 2, 9], {0: (0, 10), 1: (0, 11), 2: (1, 3), 3: (1, 4), 4: (1, 5)}),  # more rows than there are
+    ([2, 4, 5], {2: (0, 10), 3: (0, 11), 4: (1, 9)}),                        # rows in front of the first request
+    ([0, 5, 3], {0: (0, 7), 1: (0, 8), 2: (0, 9)}),                          # offsets that fall: none from cu[R] on
+    ([3, 1, 5], {1: (1, 6), 2: (1, 7), 3: (1, 8), 4: (1, 9)})])
+def test_append_offsets_that_do_not_fit_the_rows(kvs, cu, written):
+    """Rows go where the offsets say or nowhere, never over older tokens, and the status word says so."""
+    k, v, table, n = ref.make([12, 10], 2, 16, seed=3, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    wk, wv = k.clone(), v.clone()
+    Kn, Vn = torch.randn(2, 5, 2, D, device=DEV).to(torch.bfloat16)
+    for t, (r, i) in written.items():
+        wk[int(table[r, 0]), :, i], wv[int(table[r, 0]), :, i] = Kn[t], Vn[t]
+    st = _status()
+    kvs.paged_append(cache, Kn, Vn, torch.tensor(cu, dtype=torch.int32, device=DEV), dev_status=st)
+    assert torch.equal(_bits(k), _bits(wk)) and torch.equal(_bits(v), _bits(wv))
+    assert int(st) == (kvs.KVS_OK if cu == [0, 5, 3] else kvs.KVS_EBOUNDS)
+
+
 def test_append_many_requests(kvs):
     """More requests than a warp's search step, with runs of empty ones."""
     rng = np.random.default_rng(5)
