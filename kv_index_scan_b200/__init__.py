@@ -883,7 +883,7 @@ def paged_evict(cache: PagedKV, mass: torch.Tensor, budget: int, sinks: int = 0,
     po = pp if pos_out is None else cache._state("pos_out", pos_out, torch.int32)
     sp = None if seen is None else _need("seen", seen, cache._r_shape, torch.int32, dev).data_ptr()
     no = (cache.n if n_out is None else _need("n_out", n_out, cache._r_shape, torch.int32, dev)).data_ptr()
-    _require(budget >= 1, "budget must be at least 1")
+    _require(1 <= budget <= 1 << 30, f"budget must be from 1 to 2^30, got {budget}")
     if src is None:
         src = torch.empty(cache.R, cache.G, budget, dtype=torch.int32, device=dev)
     else:

@@ -194,6 +194,7 @@ kvs_status kvs_paged_evict(const kvs_paged_evict_args* a, void* ws, size_t ws_by
                   static_cast<int64_t>(a->sinks) + a->recent <= a->budget,
               KVS_EINVAL, "kvs_paged_evict: budget=%d sinks=%d recent=%d (sinks + recent <= budget)", a->budget,
               a->sinks, a->recent);
+  KVS_REQUIRE(a->budget <= (1 << 30), KVS_EUNSUPPORTED, "kvs_paged_evict: budget=%d (at most 2^30)", a->budget);
   const size_t need = paged_evict_ws_bytes(a->kv->R, a->kv->G, a->budget);
   KVS_REQUIRE(ws && ws_bytes >= need, KVS_EWORKSPACE, "kvs_paged_evict: workspace %zu < %zu bytes", ws_bytes, need);
   KVS_REQUIRE(aligned16(ws), KVS_EINVAL, "kvs_paged_evict: the workspace must be 16-byte aligned");

@@ -194,3 +194,12 @@ def test_prompt_workspace_bound_of_many_queries(kvs):
     for bad in ((0, 8, 4, 9, 65536, 0, 0), (1, 0, 4, 9, 65536, 0, 0), (1, 8, 0, 9, 65536, 0, 0), (1, 8, 9, 9, 65536, 0, 0),
                 (1, 8, 4, 0, 65536, 0, 0)):
         assert bound(*bad) == 0
+
+
+@pytest.mark.parametrize("budget", [(1 << 30) + 1, 2 ** 31 - 1])
+def test_evict_budgets_beyond_any_cache_are_refused(kvs, budget):
+    """Slots are counted in 32 bits, and a block's steps beyond the last: a budget near 2^31 would wrap."""
+    kv = _kv(kvs)
+    a = kvs.PagedEvictArgsC(ctypes.pointer(kv), 4096, None, None, budget, 0, 0, 4096, None, 4096, 4096)
+    assert kvs._lib.kvs_paged_evict(ctypes.byref(a), None, 0, None, None) == kvs.KVS_EUNSUPPORTED
+    assert b"budget" in kvs._lib.kvs_last_error()
