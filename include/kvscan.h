@@ -496,7 +496,9 @@ KVS_API kvs_status kvs_paged_append(const kvs_paged_kv* kv, const uint16_t* Knew
  * visible token mass_out[j] = mass[j] + sum_h softmax(l)_hj; the other entries
  * of mass_out stay as they are. mass_out may be mass itself, or not overlap it.
  * The softmax, the sums and the weights are f32; the products take q, K and V
- * exactly and the weights to 24 bits.
+ * exactly and the weights to 24 bits. Rows that are not visible have no influence,
+ * whatever they hold; a value of a visible V row that is not finite makes that
+ * channel not finite (an infinity may become NaN), a K row all of them.
  * Workspace: kvs_paged_decode_workspace_size(R, G, H, weights ? max_pages *
  * page : 0), independent of the lengths otherwise. */
 typedef struct {
@@ -539,8 +541,8 @@ KVS_API kvs_status kvs_selftest_paged_decode_timeout(const kvs_paged_decode_args
  * The softmax and all sums are f32; the weights are rounded to bf16 for the
  * product with V, and out once at the end. K and V rows that a query does not
  * see have no influence on it, whatever they hold; a value of a V row that is not
- * finite makes that channel of the queries that see the row not finite, a K row
- * all of theirs.
+ * finite makes that channel of the queries that see the row not finite (an infinity
+ * may become NaN), a K row all of theirs.
  * Workspace: kvs_paged_prompt_workspace_size(R, G, H, T, max_pages * page, window,
  * sinks), which is 0 where there are queries enough to occupy the GPU; fewer are
  * split over the tokens they see, and the parts joined. So it does not grow with T:

@@ -263,6 +263,33 @@ def test_decode_nothing_seen(kvs, R):
     assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
 
 
+@pytest.mark.parametrize("qdt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("window", [0, 300])
+def test_decode_values_that_are_not_finite_stay_in_their_channels(kvs, qdt, window):
+    """NaN and infinities in single values of V rows that are seen: those channels are not finite, all others are
+    bit for bit what they are without; in rows that are not seen they have no effect. A K row that is not finite
+    takes all channels of its request and head."""
+    lens = [700, 65, 9000]
+    k, v, table, n = ref.make(lens, 2, 16, seed=71, poison=False)
+    cache = kvs.PagedKV(k, v, table, n)
+    q = torch.randn(3, 2, 5, D, device=DEV).to(qdt)
+    want, wl = kvs.paged_decode_attn(q, cache, window)
+    bad = torch.zeros(3, 2, D, dtype=torch.bool, device=DEV)
+    for i, (r, g, j, d) in enumerate([(0, 0, 0, 3), (0, 0, 650, 4), (0, 1, 399, 70), (0, 1, 400, 71), (1, 0, 64, 127),
+                                      (2, 1, 8999, 0), (2, 1, 8700, 1), (2, 1, 8699, 2), (2, 0, 4000, 64)]):
+        v[int(table[r, j // 16]), g, j % 16, d] = (float("nan"), float("inf"), -float("inf"))[i % 3]
+        bad[r, g, d] |= not window or j >= lens[r] - window
+    out, lse = kvs.paged_decode_attn(q, cache, window)
+    assert torch.equal(~torch.isfinite(out), bad.unsqueeze(2).expand_as(out)) and torch.equal(lse, wl)
+    ok = ~bad.unsqueeze(2).expand_as(out)
+    assert torch.equal(out[ok], want[ok])
+    k[int(table[1, 60 // 16]), 1, 60 % 16, 9] = float("nan")
+    out2, _ = kvs.paged_decode_attn(q, cache, window)
+    assert bool(torch.isnan(out2[1, 1]).all())
+    out2[1, 1] = out[1, 1]
+    assert torch.equal(torch.isfinite(out2), torch.isfinite(out)) and torch.equal(out2[ok], out[ok])
+
+
 def test_decode_extreme_logits(kvs):
     """Logits from -3e4 to 3e4 and equal ones: the running maximum carries every one."""
     lens = [700, 700]
@@ -1030,6 +1057,50 @@ def test_evict_stream_and_graph(kvs):
                 if i == 0:
                     assert torch.equal(a[r, g], src[r, g])
         mass.uniform_()
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_evict_replays_move_rows(kvs, in_place):
+    """A captured eviction, replayed on other lengths, places and weights: moved K and V rows, weights, places and
+    lengths, each against the definition."""
+    G, page, budget, sinks, recent = 2, 16, 130, 3, 20
+    k, v, table, n = ref.make([400, 400, 270], G, page, seed=61, poison=False)  # pages for every replay
+    cache = kvs.PagedKV(k, v, table, n)
+    mass = torch.rand(3, G, cache.cap, device=DEV)
+    pos = _perm(61)(3, G, cache.cap)
+    seen = n.clone()
+    mo, po, no = (mass, pos, n) if in_place else (torch.full_like(mass, -1.0), torch.full_like(pos, -1), n.clone())
+    src = torch.empty(3, G, budget, dtype=torch.int32, device=DEV)
+    st = _status()
+    good = [t.clone() for t in (k, v, mass, pos, n)]
+    call = dict(sinks=sinks, recent=recent, pos=pos, seen=seen, src=src, mass_out=mo, pos_out=po, n_out=no, dev_status=st)
+    kvs.paged_evict(cache, mass, budget, **call)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvs.paged_evict(cache, mass, budget, **call)
+    for t, x in zip((k, v, mass, pos, n), good):
+        t.copy_(x)
+    for i, lens in enumerate(([400, 400, 90], [131, 130, 129], [0, 399, 260])):
+        n.copy_(torch.tensor(lens))
+        seen.copy_(torch.tensor(lens) + 50 * i)
+        mass.uniform_()
+        pos.copy_(_perm(62 + i)(3, G, cache.cap))
+        before = [t.clone() for t in (k, v, mass, pos)]
+        graph.replay()
+        wk, wv, m0, p0 = before[0].clone(), before[1].clone(), before[2], before[3]
+        assert no.tolist() == [min(x, budget) for x in lens]
+        for r, x in enumerate(lens):
+            for g in range(G):
+                want = ref.evict(m0[r, g].cpu().numpy(), p0[r, g].cpu().numpy(), x, x + 50 * i, budget, sinks, recent)
+                assert np.array_equal(src[r, g, :len(want)].cpu().numpy(), want) and bool((src[r, g, len(want):] == -1).all())
+                w = torch.from_numpy(want).to(DEV)
+                assert torch.equal(mo[r, g, :len(want)], m0[r, g, w]) and torch.equal(po[r, g, :len(want)], p0[r, g, w])
+                for b in np.nonzero(want != np.arange(len(want)))[0]:
+                    a, b = int(want[b]), int(b)
+                    pa, pb = int(table[r, a // page]), int(table[r, b // page])
+                    wk[pb, g, b % page] = before[0][pa, g, a % page]
+                    wv[pb, g, b % page] = before[1][pa, g, a % page]
+        assert torch.equal(_bits(k), _bits(wk)) and torch.equal(_bits(v), _bits(wv)) and int(st) == 0
 
 
 # ----------------------------------------------------------------------------- all together
