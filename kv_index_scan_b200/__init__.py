@@ -595,11 +595,6 @@ def _need(name: str, t, shape, dtype, dev):
     return t
 
 
-def _ws_args(ws):
-    """A workspace's pointer and size; None where the library asks for none (or refuses the call's sizes)."""
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
-
-
 def _check_ws(ws, dev):
     if not (ws.device == dev and ws.dtype is torch.uint8 and ws.is_contiguous()):
         raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
@@ -622,23 +617,6 @@ def _counts(**values):
             raise ValueError(f"{name} must be an int from 0 to 2^31 - 1, got {v!r}")
 
 
-class _Kept:
-    """An attribute whose tensor a C descriptor points to: assigning another one would leave the descriptor with
-    the memory of the first, so it is refused (`x.n += 1` assigns the same tensor, and is not)."""
-
-    def __init__(self, name: str):
-        self.name = name
-
-    def __get__(self, obj, cls=None):
-        return self if obj is None else obj.__dict__[self.name]
-
-    def __set__(self, obj, t):
-        _require(obj.__dict__.get(self.name, t) is t,
-                 f"{self.name} stays the tensor it was made with: change that one in place (.copy_), or make another "
-                 "cache")
-        obj.__dict__[self.name] = t
-
-
 class PagedKV:
     """A paged K/V cache (tensors owned by torch).
 
@@ -649,7 +627,14 @@ class PagedKV:
     attributes k_pages, v_pages, table and n stay these tensors; others make another PagedKV.
     """
 
-    k_pages, v_pages, table, n = (_Kept(x) for x in ("k_pages", "v_pages", "table", "n"))
+    _KEPT = frozenset(("k_pages", "v_pages", "table", "n"))
+
+    def __setattr__(self, name, value):
+        # the C descriptor points to these tensors' memory (`x.n += 1` assigns the same tensor)
+        if name in self._KEPT and self.__dict__.get(name, value) is not value:
+            raise ValueError(f"{name} stays the tensor it was made with: change that one in place (.copy_), or make "
+                             "another cache")
+        object.__setattr__(self, name, value)
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, n: torch.Tensor):
         for name, t, dt, dims in (("k_pages", k_pages, torch.bfloat16, 4), ("v_pages", v_pages, torch.bfloat16, 4),
@@ -760,8 +745,8 @@ def paged_decode_attn(q: torch.Tensor, cache: PagedKV, window: int = 0, sinks: i
     a = PagedDecodeArgsC(cache._ref, q.data_ptr(), KVS_BF16 if bf16 else KVS_F32, H, window, sinks,
                          1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), lse.data_ptr(), mp, mo)
     st_ptr = None if dev_status is None else _status_ptr(dev_status, dev)
-    _check(_lib.paged_decode_attn(ctypes.byref(a), *_ws_args(ws), st_ptr, _raw_stream(dev)),
-           "paged_decode_attn")
+    wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+    _check(_lib.paged_decode_attn(ctypes.byref(a), wp, wn, st_ptr, _raw_stream(dev)), "paged_decode_attn")
     return out, lse
 
 
@@ -772,11 +757,12 @@ def selftest_paged_decode_timeout(q: torch.Tensor, cache: PagedKV, warp: int, wa
     dev = cache.device
     with _on(dev, stream):
         H = q.shape[2]
+        _require(1 <= H <= 8, f"1 to 8 query heads a KV head, got {H}")
         _need("q", q, (cache.R, cache.G, H, cache.D), torch.bfloat16, dev)
         out = torch.empty(q.shape, dtype=torch.float32, device=dev)
         ws = paged_decode_workspace(cache, H)
         a = PagedDecodeArgsC(cache._ref, q.data_ptr(), KVS_BF16, H, 0, 0, 1.0, out.data_ptr(), None, None, None)
-        _check(_lib.kvs_selftest_paged_decode_timeout(ctypes.byref(a), *_ws_args(ws), warp, wait_cycles,
+        _check(_lib.kvs_selftest_paged_decode_timeout(ctypes.byref(a), ws.data_ptr(), ws.numel(), warp, wait_cycles,
                                                       _status_ptr(dev_status, dev), _raw_stream(dev)),
                "kvs_selftest_paged_decode_timeout")
 
@@ -838,8 +824,8 @@ def paged_prompt_attn(q: torch.Tensor, cu: torch.Tensor, cache: PagedKV, window:
     else:
         _check_ws(ws, dev)
     st_ptr = None if dev_status is None else _status_ptr(dev_status, dev)
-    _check(_lib.paged_prompt_attn(ctypes.byref(a), *_ws_args(ws), st_ptr, _raw_stream(dev)),
-           "paged_prompt_attn")
+    wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+    _check(_lib.paged_prompt_attn(ctypes.byref(a), wp, wn, st_ptr, _raw_stream(dev)), "paged_prompt_attn")
     return out, lse
 
 
@@ -883,7 +869,8 @@ def paged_evict(cache: PagedKV, mass: torch.Tensor, budget: int, sinks: int = 0,
     po = pp if pos_out is None else cache._state("pos_out", pos_out, torch.int32)
     sp = None if seen is None else _need("seen", seen, cache._r_shape, torch.int32, dev).data_ptr()
     no = (cache.n if n_out is None else _need("n_out", n_out, cache._r_shape, torch.int32, dev)).data_ptr()
-    _require(1 <= budget <= 1 << 30, f"budget must be from 1 to 2^30, got {budget}")
+    if not 1 <= budget <= 1 << 30:
+        raise ValueError(f"budget must be from 1 to 2^30, got {budget}")
     if src is None:
         src = torch.empty(cache.R, cache.G, budget, dtype=torch.int32, device=dev)
     else:
@@ -894,6 +881,6 @@ def paged_evict(cache: PagedKV, mass: torch.Tensor, budget: int, sinks: int = 0,
         _check_ws(ws, dev)
     a = PagedEvictArgsC(cache._ref, mp, pp, sp, budget, sinks, recent, mo, po, no, src.data_ptr())
     st_ptr = None if dev_status is None else _status_ptr(dev_status, dev)
-    _check(_lib.kvs_paged_evict(ctypes.byref(a), *_ws_args(ws), st_ptr, _raw_stream(dev)),
-           "kvs_paged_evict")
+    wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+    _check(_lib.kvs_paged_evict(ctypes.byref(a), wp, wn, st_ptr, _raw_stream(dev)), "kvs_paged_evict")
     return src

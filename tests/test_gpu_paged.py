@@ -494,6 +494,18 @@ def test_no_heads_and_no_pages_are_refused(kvs):
             kvs.PagedKV(none, none, table, n)
 
 
+def test_a_cache_of_no_requests_is_refused(kvs):
+    k, v, table, n = ref.make([20], 2, 16, seed=1)
+    cache = kvs.PagedKV(k, v, table[:0], n[:0])
+    none = torch.empty(0, 8, D, dtype=torch.bfloat16, device=DEV)
+    for call in (lambda: kvs.paged_decode_attn(none.view(0, 2, 4, D), cache),
+                 lambda: kvs.paged_prompt_attn(none, torch.zeros(1, dtype=torch.int32, device=DEV), cache),
+                 lambda: kvs.paged_append(cache, none[:, :2], none[:, :2]),
+                 lambda: kvs.paged_evict(cache, torch.zeros(0, 2, cache.cap, device=DEV), 8)):
+        with pytest.raises(kvs.KvsError):
+            call()
+
+
 # ----------------------------------------------------------------------------- prompt
 
 def _prompt(kvs, lens, new, G, H, page, window, sinks, seed=0, pad=3, layout="head", poison=True):
