@@ -591,6 +591,9 @@ KVS_API kvs_status kvs_selftest_paged_prompt_timeout(const kvs_paged_prompt_args
  *   input itself (in place), or not overlap it.
  *   src (required) int32 [R][G][budget]: the slot that slot j's token was in,
  *   -1 from n_out[r] on.
+ * The weights come from paged_decode_attn (a new token's is 0, and a prompt adds
+ * none): cutting a prompt before its first decode steps needs weights from
+ * elsewhere, or keeps the sinks, the recent and of the others the oldest.
  * budget in 1 .. 2^30, sinks, recent >= 0, sinks + recent <= budget. Pages behind
  * n_out[r] are free afterwards. A page that moves rows must not be shared by
  * two requests, nor be read by a call that runs at the same time.

@@ -10,7 +10,9 @@
 //    A row that lies inside one run is finished there; of a cut row, each
 //    block leaves its maximum, sum and unnormalised output, and a second
 //    kernel joins them. A run cuts at most the row it begins in and the row it
-//    ends in, so the scratch is two partial rows a block, independent of n.
+//    ends in, so the scratch is two partial rows a block, independent of n. That
+//    kernel has a block for every row, or, with more rows than SMs, for every
+//    run's end.
 //  * One warp loads: a TMA copy per page and pool brings up to 64 tokens of one
 //    head (both 128-byte halves, swizzled) into a ring of three 32 KB stages,
 //    with what the consumers need to know about the unit beside it. Two blocks
@@ -26,10 +28,14 @@
 //    whatever lies there (NaN too) must not meet a weight of zero.
 //  * With weights wanted, the logits go to scratch (4 H bytes a token beside
 //    the 512 read) and the join turns them into weights, once the row's
-//    log-sum-exp is known.
-// Measured: 16 requests of 16K to 128K tokens, 3.70 GB: 0.54 to 0.62 ms (5.99 to
-// 6.9 TB/s of the 6.55 a copy reaches); 32 requests seeing 4100 tokens each, 8
-// heads: 88 us (5.7 TB/s); one request of 4096 tokens: 10.8 us, 2.5 of them the join.
+//    log-sum-exp is known (a kernel of its own with more than four rows an SM).
+//  * Every wait is bounded; one that runs out writes KVS_ETIMEOUT. The computing
+//    warps meet at a row's end, at mbarriers too: warp 0 adds up the others' parts
+//    while they go on with the next row.
+// Measured: 16 requests of 16K to 128K tokens, 3.70 GB: 0.60 to 0.61 ms (6.1 TB/s
+// of the 6.55 a copy reaches); 32 requests seeing 4100 tokens each, 8 heads: 89.5 us
+// (5.65 TB/s); 16 of 3K to 8K with weights 71.5 us; one request of 4096 tokens: 10.9
+// us, 2.5 of them the join.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -347,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
       // a new row
       if (i > 0) load_q(info.row);
       // the next row's on their way to L1 meanwhile, a line a lane (4096 rows of 256
-      // tokens: 103 us became 99)
+      // tokens: 103 us became 99, 96 since)
       if (info.row + 1 < kv.R * G && lane < H * kD * (kF32Q ? 4 : 2) / 128)
         asm volatile("prefetch.global.L1 [%0];\n" ::"l"(
             static_cast<const char*>(p.q) + static_cast<size_t>(info.row + 1) * H * kD * (kF32Q ? 4 : 2) + 128 * lane));
@@ -543,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) paged_decode_kernel(co
 constexpr int kJoinThreads = 512;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kFewBatch = 8;
-constexpr int kCutThreads = 256;  // with 77 registers a thread three blocks an SM
+constexpr int kCutThreads = 256;  // with 69 registers a thread three blocks an SM
 constexpr int kWeighThreads = 256, kWeighTokens = 1024, kWeighBlocksPerSM = 8;
 constexpr int kWeighRowsPerSM = 4;  // with more rows the weights have a kernel of their own
 constexpr int kJoinTokens = 2048;  // tokens of a row that one block turns into weights
@@ -698,7 +704,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_few_kernel(con
 // than there are rows, and most rows lie in one run and need no joining. Block b
 // joins the row that run b ends in the middle of, if the row begins in run b, and
 // sees to every gridDim.x-th of the requests that nothing is seen of. 4096 rows of
-// 256 tokens: the whole call 103 us (99 since), with a block for every row 129; 1024 rows of
+// 256 tokens: the whole call 103 us (96 since), with a block for every row 129; 1024 rows of
 // 1024 tokens 92 us, 99.
 __global__ void __launch_bounds__(kCutThreads) paged_decode_join_cut_kernel(const DecodeParams p) {
   __shared__ int64_t scan_part[kCutThreads / 32];
@@ -850,7 +856,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_weights_kernel(cons
 }
 
 // The weights alone, where another kernel has joined the rows: `share` blocks a row.
-// With weights, 4096 rows of 256 tokens: 143 us with the kernel above, 119 with this
+// With weights, 4096 rows of 256 tokens: 143 us with the kernel above, 119 (111 since) with this
 // one; 1024 rows of 1024 tokens 110 and 105; 256 rows of 1024 36 and 37.7, a launch more.
 __global__ void __launch_bounds__(kWeighThreads) paged_decode_weigh_kernel(const DecodeParams p, int share) {
   __shared__ float s_lse2[8];

@@ -24,8 +24,8 @@
 //     flight per warp.
 // Ties at the cut go to the lower slots: only then the tied keys are ranked too.
 // Bound by the moved rows' bytes, for small moves by the latency of the steps:
-// 8 prompts of 16K to 64K tokens cut to 4096 (64 rows, 246,000 moves) take 82 us,
-// 47 of them the moves at 5.4 TB/s; 128 rows of 4097 slots, one move each, 14.8 us.
+// 8 prompts of 16K to 64K tokens cut to 4096 (64 rows, 246,000 moves) take 68 us,
+// 38 of them the moves; 128 rows of 4097 slots, one move each, 12.5 us.
 #include <cooperative_groups.h>
 
 #include "paged.cuh"
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_evict_kernel(EvictParams p)
   const int32_t* movers = p.movers + static_cast<size_t>(u) * b;
   const bool isv = lane >= 16;
   uint16_t* pool = (isv ? p.kv.V : p.kv.K) + 8 * (lane & 15);
-  // moves k0 + x * C * kWarps ...: spread so that few moves reach every warp
+  // a run of up to 32 moves a warp, shorter where that lets few moves reach every warp
   const int workers = C * kWarps, me = rank * kWarps + warp;
   const int chunk = min(32, (count + workers - 1) / workers);
   for (int k0 = me * chunk; k0 < count; k0 += workers * chunk) {
@@ -343,7 +343,7 @@ kvs_status paged_evict_launch(const kvs_paged_evict_args* a, void* ws, int32_t* 
   // blocks a row: enough to occupy two on every SM, each with at least so many
   // slots of the longest row there may be. Where few rows can move, the cluster's
   // barriers cost more than half a run saves (128 rows of 4097 slots, budget 4096:
-  // one block a row 13.8 us, two 17.7); where many can, the moves want the blocks
+  // one block a row 12.5 us, two 13.5 to 15); where many can, the moves want the blocks
   // (2 rows of 8765 slots cut to 1409: two blocks a row 21.4 us, four 14.8; 8 rows
   // of 8192 cut to 4096: 29.5 and 22.7).
   const int64_t cap = static_cast<int64_t>(a->kv->max_pages) * a->kv->page;

@@ -36,11 +36,16 @@
 //    search for them takes 1% of a long prompt's time and 3% of short items' (64
 //    prompts of 300 tokens over 300: 199 us and 205 with it); without it a NaN
 //    reached the queries in front of its token.
-// Measured: 8192 tokens of 32 heads over 8 KV heads, causal, 0.55 TFLOP: 0.44 to
-// 0.50 ms by the clocks that the power cap leaves (1.10 to 1.25 PFLOP/s; a large
-// library product reaches 1.66 in a burst and 1.40 for seconds); 2048 tokens over
-// 32768 with a window of 4096: 144 us (0.96 PFLOP/s; 256 items for 148 SMs); 128
-// tokens 9.4 us; 4 tokens over 28676 37 us (359 before the split). The products
+//  * The weights are rounded to bf16: the tensor cores take both operands in one
+//    16-bit type, and a second product for what the rounding leaves would be half
+//    as much tensor time again (full 24 bits is the decode form's choice, where
+//    memory bounds). It costs an error of 2.1e-3 to 2.3e-3 against 64 bits, where
+//    rounding the exact output to bf16 alone gives 1.6e-3 to 1.7e-3.
+// Measured: 8192 tokens of 32 heads over 8 KV heads, causal, 0.55 TFLOP: 0.50 ms
+// under the power cap (1.09 PFLOP/s; a large library product reaches 1.66 in a burst
+// and 1.40 for seconds), 0.43 before it sets in; 2048 tokens over 32768 with a window
+// of 4096: 158 us (0.87 PFLOP/s; 256 items for 148 SMs); 128 tokens 9.7 us; 4 tokens
+// over 28676 40 us (359 before the split). The products
 // with their loads alone take 0.32 and 0.09 ms: what is left is each row tile's
 // chain from S through the softmax to the next S.
 // Every wait is bounded; one that runs out writes KVS_ETIMEOUT, and the block
@@ -999,7 +1004,9 @@ int64_t longest_item(int H, int64_t cap, int window, int sinks) {
 // with t tiles in the longest item that there may be, a round of whole items
 // takes t + 3.5, one of n pieces t / n + 5, and the join 4 (8 heads, 4 tokens over
 // 28676: 359 us whole, 37 in 18 pieces; 2 heads, 1024 tokens: 20.6 whole, 23.1 in
-// two): the number with the least sum of rounds.
+// two): the number with the least sum of rounds. The longest item that there may be
+// is the table's width: a table much wider than what it holds splits items that need
+// it not (128 tokens 9.2 us and 18 from 4096 slots on, 1024 tokens 22 and 71 at 131072).
 int pieces_of(int R, int G, int H, int T, int64_t cap, int window, int sinks) {
   const int64_t items = most_items(R, G, H, T), sms = sm_count(), t = longest_item(H, cap, window, sinks);
   int best = 1;
